@@ -164,7 +164,7 @@ def _slots(case, seed):
     slots = table[:, i // page] * page + i % page
     if case["pad"]:
         slots[::2, n - case["pad"]:] = -1
-    return slots.contiguous(), n_pages
+    return slots.int().contiguous(), n_pages
 
 
 def _prompt(case, seed):
