@@ -9,11 +9,14 @@ Names follow the C ABI: kvpop_cache_bytes, kvpop_create, kvpop_prefill,
 kvpop_decode_step, kvpop_inspect, kvpop_get_layout, kvpop_get_error,
 kvpop_clear_error, kvpop_debug_poison_error, kvpop_destroy,
 kvpop_status_string.  `KVPopCache` bundles a handle with its device buffer.
+The paged cache's calls (kvpop_paged_*) are methods of `KVPopPagedCache`;
+`qk_norm_rope` is kvpop_qk_norm_rope.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -34,6 +37,8 @@ KVPOP_NOALLOC_SCRATCH_BYTES = 16 << 20   # static split-K buffer behind decode_s
 
 KVPOP_DTYPE_F32 = 0
 KVPOP_DTYPE_BF16 = 1
+KVPOP_CACHE_NATIVE = 0
+KVPOP_CACHE_E4M3 = 1
 KVPOP_FLAG_EXTERNAL_SCORES = 1
 KVPOP_FLAG_DEBUG_CHECKS = 2
 
@@ -50,6 +55,9 @@ EXPORTED_SYMBOLS = (
     "kvpop_destroy", "kvpop_status_string", "kvpop_decode_step_noalloc",
     "kvpop_prefill_attention_workspace_bytes", "kvpop_prefill_attention", "kvpop_prefill_with_attention",
     "kvpop_debug_set_hook", "kvpop_prefill_attention_from_cutoffs",
+    "kvpop_qk_norm_rope", "kvpop_paged_bytes", "kvpop_paged_create", "kvpop_paged_append",
+    "kvpop_paged_append_qkv", "kvpop_paged_gather", "kvpop_paged_attend", "kvpop_paged_get_layout",
+    "kvpop_paged_get_error", "kvpop_paged_clear_error", "kvpop_paged_destroy",
 )
 
 
@@ -90,12 +98,30 @@ class kvpop_layout_info(ctypes.Structure):
     ]
 
 
+class kvpop_paged_config(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "n_layers", "n_q_heads", "n_kv_heads", "head_dim", "page_size", "n_pages", "max_batch", "dtype",
+        "cache_format")]
+
+
+class kvpop_paged_layout_info(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_size_t) for name in (
+        "pages_offset", "pages_layer_stride", "scales_offset", "scales_layer_stride")]
+
+
+# kvpop_rows, kvpop_rope and kvpop_attend_options, packed for one call each
+_pack_rows = struct.Struct("@Pqqq").pack
+_pack_rope = struct.Struct("@PPPffii").pack
+_pack_attend_options = struct.Struct("@ffi").pack
+
+
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"libkvpop.so not built at {path}: run "
                           "`python fixed_budget_kv_kvpop_b200/csrc/build.py` (no CPU fallback exists)")
     lib = ctypes.CDLL(path)
     P, I32, U32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t
+    I64 = ctypes.c_int64
     sig = {
         "kvpop_cache_bytes": ([ctypes.POINTER(kvpop_config), ctypes.POINTER(SZ)], ctypes.c_int),
         "kvpop_create": ([ctypes.POINTER(kvpop_config), P, SZ, ctypes.POINTER(P)], ctypes.c_int),
@@ -116,6 +142,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kvpop_prefill_with_attention": ([P, I32, P, P, P, I32, P, P, P, P, SZ, P], ctypes.c_int),
         "kvpop_debug_set_hook": ([P, I32], ctypes.c_int),
         "kvpop_prefill_attention_from_cutoffs": ([P, I32, P, P, P, I32, P, P, P, SZ, P], ctypes.c_int),
+        "kvpop_qk_norm_rope": ([I32, I32, I32, I32, P, I32, I32, P, P, P, P, P, P], ctypes.c_int),
+        "kvpop_paged_bytes": ([ctypes.POINTER(kvpop_paged_config), ctypes.POINTER(SZ)], ctypes.c_int),
+        "kvpop_paged_create": ([ctypes.POINTER(kvpop_paged_config), P, SZ, ctypes.POINTER(P)], ctypes.c_int),
+        "kvpop_paged_append": ([P, I32, P, P, P, I32, I32, P], ctypes.c_int),
+        "kvpop_paged_append_qkv": ([P, I32, P, P, P, P, P, P, P, I32, I32, P], ctypes.c_int),
+        "kvpop_paged_gather": ([P, I32, P, I64, I32, P, I32, I32, P, P, P], ctypes.c_int),
+        "kvpop_paged_attend": ([P, I32, P, P, I64, I32, P, I32, P, P, P, P], ctypes.c_int),
+        "kvpop_paged_get_layout": ([P, ctypes.POINTER(kvpop_paged_layout_info)], ctypes.c_int),
+        "kvpop_paged_get_error": ([P, ctypes.POINTER(I32)], ctypes.c_int),
+        "kvpop_paged_clear_error": ([P, P], ctypes.c_int),
+        "kvpop_paged_destroy": ([P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -415,3 +452,282 @@ class KVPopCache:
     def set_test_hook(self, hook: int):
         """Failure injection of a KVPOP_TEST_HOOKS build (kvpop_debug_set_hook)."""
         _check(self._lib.kvpop_debug_set_hook(self.handle, hook), "kvpop_debug_set_hook")
+
+
+# ---- heads of new tokens, and the paged (full) cache ----
+
+def _stream_on(device, stream) -> Optional[int]:
+    """The given stream, or `device`'s current one (which need not be the current device's)."""
+    if stream is None:
+        import torch
+        stream = torch.cuda.current_stream(device)
+    return stream.cuda_stream or None
+
+
+def _rows(t, name: str, shape, dtype, device, written: bool = False) -> bytes:
+    """A kvpop_rows of `t`, rows [batch][token][head][head_dim] with the last
+    dimension contiguous: any strides of whole 16 bytes.  Raises ValueError on
+    anything else; the C ABI sees only addresses."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name}: on {t.device}, expected the cuda device {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    sb, st, sh, sd = t.stride()
+    b, n, h, _ = shape
+    unit = 16 // t.element_size()
+    bad = sd != 1 or (b > 1 and sb % unit) or (n > 1 and st % unit) or (h > 1 and sh % unit) or t.data_ptr() % 16
+    if bad and b and n:
+        raise ValueError(f"{name}: strides {t.stride()} at {t.data_ptr():#x}: rows must be contiguous and start on "
+                         "16 bytes")
+    if written and b and n and ((b > 1 and not sb) or (n > 1 and not st) or (h > 1 and not sh)):
+        raise ValueError(f"{name}: an expanded tensor cannot be written")
+    return _pack_rows(t.data_ptr(), sb, st, sh)
+
+
+def _ints(t, name: str, shape, device) -> int:
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.shape != shape or t.device != device \
+            or not t.is_contiguous():
+        what = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
+        raise ValueError(f"{name}: expected a contiguous int32 tensor {tuple(shape)} on {device}, got {what}")
+    return t.data_ptr()
+
+
+class Rope:
+    """Norm weights and rotation of query and key heads (kvpop_rope); keeps
+    its tensors alive.  Made by make_rope."""
+
+    def __init__(self, inv_freq, q_weight, k_weight, eps, scale, interleaved):
+        self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight
+        self.device = inv_freq.device
+        self.rot_dim = 2 * inv_freq.numel()
+        self.head_dim = next((w.numel() for w in (q_weight, k_weight) if w is not None), None)
+        self.packed = _pack_rope(_ptr(q_weight) or 0, _ptr(k_weight) or 0, inv_freq.data_ptr(), eps, scale,
+                                 self.rot_dim, int(bool(interleaved)))
+
+
+def make_rope(inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6, scale: float = 1.0,
+              interleaved: bool = False) -> Rope:
+    """inv_freq: device fp64 [rot_dim / 2], the angle of pair i at position p
+    being p * inv_freq[i]; rot_dim a multiple of 8 up to head_dim (an empty
+    tensor: no rotation).  q_weight, k_weight: device fp32 [head_dim] norm
+    weights, or None for heads that are not normalised.  eps is added to the
+    mean square; scale multiplies cosine and sine.  interleaved: pairs
+    (2i, 2i + 1) instead of (i, i + rot_dim / 2)."""
+    import torch
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.device.type != "cuda":
+        raise ValueError("inv_freq: expected a cuda tensor")
+    if inv_freq.dim() != 1 or inv_freq.numel() % 4:
+        raise ValueError(f"inv_freq: shape {tuple(inv_freq.shape)}, expected one dimension, a multiple of 4 long")
+    check_tensor(inv_freq, "inv_freq", inv_freq.shape, torch.float64, inv_freq.device)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            n = w.numel() if isinstance(w, torch.Tensor) else 0
+            check_tensor(w, name, (n,), torch.float32, inv_freq.device)
+            if w.data_ptr() % 16:
+                raise ValueError(f"{name}: must start on 16 bytes")
+    if q_weight is not None and k_weight is not None and q_weight.numel() != k_weight.numel():
+        raise ValueError("q_weight and k_weight: different lengths")
+    return Rope(inv_freq, q_weight, k_weight, eps, scale, interleaved)
+
+
+def _check_rope(rope, head_dim, device):
+    if not isinstance(rope, Rope):
+        raise ValueError(f"rope: expected a Rope (make_rope), got {type(rope).__name__}")
+    if rope.device != device:
+        raise ValueError(f"rope: on {rope.device}, the rows are on {device}")
+    if rope.head_dim not in (None, head_dim):
+        raise ValueError(f"rope: weights of {rope.head_dim} elements, head_dim is {head_dim}")
+
+
+def qk_norm_rope(rope: Rope, q, k, positions, q_out, k_out, stream=None) -> None:
+    """Norm and rotation of query and key heads (kvpop_qk_norm_rope).  q,
+    q_out: [batch][tokens][q heads][head_dim]; k, k_out: the same with the KV
+    heads; any strides of whole 16 bytes (views of a projection's output,
+    transposed views of head-major buffers), q_out = q and k_out = k among
+    them.  positions: int32 [batch][tokens]."""
+    import torch
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.device.type != "cuda":
+        raise ValueError("q: expected a cuda tensor [batch][tokens][heads][head_dim]")
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k: expected a cuda tensor [batch][tokens][heads][head_dim]")
+    dtype, device, qs = q.dtype, q.device, q.shape
+    b, n, hq, d = qs
+    hkv = k.shape[2]
+    ks = torch.Size((b, n, hkv, d))
+    _check_rope(rope, d, device)
+    _check(lib.kvpop_qk_norm_rope(dtype_code(dtype), d, hq, hkv, rope.packed, b, n,
+                                  _rows(q, "q", qs, dtype, device), _rows(k, "k", ks, dtype, device),
+                                  _ints(positions, "positions", (b, n), device),
+                                  _rows(q_out, "q_out", qs, dtype, device, True),
+                                  _rows(k_out, "k_out", ks, dtype, device, True), _stream_on(device, stream)),
+           "kvpop_qk_norm_rope")
+
+
+_CACHE_FORMATS = {"native": KVPOP_CACHE_NATIVE, "e4m3": KVPOP_CACHE_E4M3}
+
+
+def make_paged_config(*, n_layers, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_batch, dtype="bf16",
+                      cache="native") -> kvpop_paged_config:
+    """cache: 'native' (rows held in dtype) or 'e4m3' (8 bits and one fp32
+    scale per key row and per value row; dtype bf16)."""
+    if cache not in _CACHE_FORMATS:
+        raise ValueError(f"unknown cache format {cache!r}: use one of {sorted(_CACHE_FORMATS)}")
+    return kvpop_paged_config(n_layers, n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_batch,
+                              dtype_code(dtype), _CACHE_FORMATS[cache])
+
+
+def paged_bytes(cfg: kvpop_paged_config, library=None) -> int:
+    n = ctypes.c_size_t(0)
+    _check((library or lib).kvpop_paged_bytes(ctypes.byref(cfg), ctypes.byref(n)), "kvpop_paged_bytes")
+    return n.value
+
+
+class KVPopPagedCache:
+    """A paged cache: a handle plus the device buffer it lives in (allocated
+    with torch).  Calls on one object must be ordered on one stream, or by
+    events."""
+
+    def __init__(self, cfg: kvpop_paged_config, device=None, library=None):
+        import torch
+        self.cfg = cfg
+        self._lib = library or lib
+        self.nbytes = paged_bytes(cfg, self._lib)
+        self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device or "cuda")
+        self.device = self.buffer.device
+        base = self.buffer.data_ptr()
+        self._off = (-base) % 256
+        self.handle = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            _check(self._lib.kvpop_paged_create(ctypes.byref(cfg), ctypes.c_void_p(base + self._off), self.nbytes,
+                                                ctypes.byref(self.handle)), "kvpop_paged_create")
+        self.dtype = _torch_dtype(cfg.dtype)
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h:
+            self._lib.kvpop_paged_destroy(h)
+            self.handle = None
+
+    def _kv_shape(self, t, name):
+        import torch
+        if not isinstance(t, torch.Tensor) or t.dim() != 4:
+            raise ValueError(f"{name}: expected a cuda tensor [batch][tokens][heads][head_dim]")
+        return torch.Size((t.shape[0], t.shape[1], self.cfg.n_kv_heads, self.cfg.head_dim))
+
+    def append(self, layer: int, k, v, slots, stream=None) -> None:
+        """Writes keys and values, [batch][tokens][KV heads][head_dim], to the
+        rows that slots (int32 [batch][tokens]: page * page_size + row;
+        negative: written nowhere) name.  No two tokens may share a slot."""
+        shape = self._kv_shape(k, "k")
+        b, n = shape[0], shape[1]
+        _check(self._lib.kvpop_paged_append(self.handle, layer, _rows(k, "k", shape, self.dtype, self.device),
+                                            _rows(v, "v", shape, self.dtype, self.device),
+                                            _ints(slots, "slots", (b, n), self.device), b, n,
+                                            _stream_on(self.device, stream)), "kvpop_paged_append")
+
+    def append_qkv(self, layer: int, rope: Rope, q, k, v, positions, slots, q_out, stream=None) -> None:
+        """qk_norm_rope and append in one launch: normalised and turned queries
+        go to q_out, keys and values to their slots."""
+        import torch
+        shape = self._kv_shape(k, "k")
+        b, n, d = shape[0], shape[1], shape[3]
+        qs = torch.Size((b, n, self.cfg.n_q_heads, d))
+        _check_rope(rope, d, self.device)
+        _check(self._lib.kvpop_paged_append_qkv(self.handle, layer, rope.packed,
+                                                _rows(q, "q", qs, self.dtype, self.device),
+                                                _rows(k, "k", shape, self.dtype, self.device),
+                                                _rows(v, "v", shape, self.dtype, self.device),
+                                                _ints(positions, "positions", (b, n), self.device),
+                                                _ints(slots, "slots", (b, n), self.device),
+                                                _rows(q_out, "q_out", qs, self.dtype, self.device, True), b, n,
+                                                _stream_on(self.device, stream)), "kvpop_paged_append_qkv")
+
+    def _table(self, page_table, lens, b):
+        import torch
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            raise ValueError("page_table: expected an int32 cuda tensor [batch][pages]")
+        width = page_table.shape[1]
+        return (_ints(page_table, "page_table", (b, width), self.device), width,
+                _ints(lens, "lens", (b,), self.device))
+
+    def gather(self, layer: int, page_table, lens, k_out, v_out, stream=None) -> None:
+        """Reads sequences back: the first lens[b] tokens of sequence b, whose
+        pages are page_table[b] (int32 [batch][pages]), go to k_out and v_out,
+        [batch][tokens][KV heads][head_dim]; rows behind them stay as they were."""
+        shape = self._kv_shape(k_out, "k_out")
+        b, n = shape[0], shape[1]
+        table, width, lens_p = self._table(page_table, lens, b)
+        _check(self._lib.kvpop_paged_gather(self.handle, layer, table, width, width, lens_p, b, n,
+                                            _rows(k_out, "k_out", shape, self.dtype, self.device, True),
+                                            _rows(v_out, "v_out", shape, self.dtype, self.device, True),
+                                            _stream_on(self.device, stream)), "kvpop_paged_gather")
+
+    def attend(self, layer: int, q, page_table, lens, out, lse=None, scale=0.0, softcap=0.0, window=0,
+               stream=None) -> None:
+        """Attention of one new token per sequence: q, out [batch][q heads]
+        [head_dim]; lse fp32 [batch][q heads] or None.  scale 0: 1 / sqrt(head_dim);
+        softcap > 0: scores become softcap * tanh(score / softcap); window > 0:
+        the last `window` tokens alone are attended."""
+        import torch
+        c = self.cfg
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q: expected a cuda tensor [batch][q heads][head_dim]")
+        b = q.shape[0]
+        shape = torch.Size((b, c.n_q_heads, c.head_dim))
+        check_tensor(q, "q", shape, self.dtype, self.device)
+        check_tensor(out, "out", shape, self.dtype, self.device)
+        if lse is not None:
+            check_tensor(lse, "lse", shape[:2], torch.float32, self.device)
+        table, width, lens_p = self._table(page_table, lens, b)
+        _check(self._lib.kvpop_paged_attend(self.handle, layer, q.data_ptr(), table, width, width, lens_p, b,
+                                            _pack_attend_options(scale, softcap, window), out.data_ptr(), _ptr(lse),
+                                            _stream_on(self.device, stream)), "kvpop_paged_attend")
+
+    def _view(self, offset, shape, dtype):
+        n = dtype.itemsize
+        for s in shape:
+            n *= s
+        start = self._off + offset
+        return self.buffer[start:start + n].view(dtype).view(shape)
+
+    def _layer_view(self, layer, offset, stride, shape, dtype):
+        if not 0 <= layer < self.cfg.n_layers:
+            raise ValueError(f"layer {layer}: the cache has {self.cfg.n_layers}")
+        return self._view(offset + layer * stride, shape, dtype)
+
+    def pages(self, layer: int):
+        """Layer `layer`'s held rows, [pages][KV heads][2 (key, value)][page_size][head_dim]: a view."""
+        import torch
+        c, lay = self.cfg, self.layout()
+        dtype = torch.float8_e4m3fn if c.cache_format == KVPOP_CACHE_E4M3 else self.dtype
+        return self._layer_view(layer, lay.pages_offset, lay.pages_layer_stride,
+                                (c.n_pages, c.n_kv_heads, 2, c.page_size, c.head_dim), dtype)
+
+    def scales(self, layer: int):
+        """The scales of layer `layer`'s rows, [pages][KV heads][2][page_size]: a view; None without them."""
+        import torch
+        c, lay = self.cfg, self.layout()
+        if c.cache_format != KVPOP_CACHE_E4M3:
+            return None
+        return self._layer_view(layer, lay.scales_offset, lay.scales_layer_stride,
+                                (c.n_pages, c.n_kv_heads, 2, c.page_size), torch.float32)
+
+    def layout(self) -> kvpop_paged_layout_info:
+        info = kvpop_paged_layout_info()
+        _check(self._lib.kvpop_paged_get_layout(self.handle, ctypes.byref(info)), "kvpop_paged_get_layout")
+        return info
+
+    def get_error(self):
+        bits = ctypes.c_int32(0)
+        st = self._lib.kvpop_paged_get_error(self.handle, ctypes.byref(bits))
+        return st, bits.value
+
+    def clear_error(self, stream=None):
+        _check(self._lib.kvpop_paged_clear_error(self.handle, _stream_on(self.device, stream)),
+               "kvpop_paged_clear_error")

@@ -381,6 +381,172 @@ int kvpop_debug_set_hook(kvpop_handle* h, int32_t hook);
  * KVPOP_ERR_INVALID_ARG on NULL. */
 int kvpop_destroy(kvpop_handle* h);
 
+/* ---------------------------------------------------------------------------
+ * Heads of new tokens, and the paged (full) cache.
+ *
+ * A model rarely prunes every layer: the layers, or the sequences, that keep
+ * every token hold them in pages.  These calls stand beside the fixed-budget
+ * ones: kvpop_qk_norm_rope makes the queries and keys that kvpop_prefill,
+ * kvpop_decode_step and the paged cache take; kvpop_paged_append and
+ * kvpop_paged_attend are kvpop_decode_append and kvpop_decode_attend without
+ * a budget; kvpop_paged_gather hands a sequence's rows to kvpop_prefill or
+ * kvpop_prefill_with_attention, which prune it.  No passage of the KVpop pages
+ * defines them.  The conventions at the top of this file hold, with one
+ * addition: a call may be made while another device than the handle's is
+ * current (the stream must belong to the handle's device). */
+
+/* Rows [batch][token][head][head_dim]: the address of the first element and
+ * the strides of the first three dimensions in elements; the last dimension is
+ * contiguous.  data must be 16-byte aligned and every stride of a dimension
+ * longer than one a multiple of 16 bytes and not negative.  A stride of 0
+ * (a broadcast) is taken for inputs only.  Rows that are written must not
+ * overlap each other, nor an input of the call, except that q_out may be q
+ * and k_out may be k (the same address and strides). */
+typedef struct kvpop_rows {
+  void* data;
+  int64_t batch_stride, token_stride, head_stride;
+} kvpop_rows;
+
+/* Norm and position rotation of query and key heads:
+ *   y = x / sqrt(mean(x^2) + eps) * weight        (skipped where weight is NULL)
+ *   (a, b) -> (a cos - b sin, b cos + a sin), angle = position * inv_freq[i]
+ * for the pairs i < rot_dim / 2: elements (i, i + rot_dim / 2), or with
+ * interleaved (2i, 2i + 1); elements from rot_dim on are not turned.  Angles
+ * are formed in fp64 (any int32 position), the rest in fp32, and the result
+ * is rounded once.  rot_scale multiplies cosine and sine (1 for plain
+ * rotation).  All pointers are device memory, read while the call runs. */
+typedef struct kvpop_rope {
+  const float* q_weight;    /* fp32 [head_dim] or NULL, 16-byte aligned */
+  const float* k_weight;    /* fp32 [head_dim] or NULL, 16-byte aligned */
+  const double* inv_freq;   /* fp64 [rot_dim / 2] */
+  float eps;                /* >= 0 */
+  float rot_scale;
+  int32_t rot_dim;          /* multiple of 8, 0 <= rot_dim <= head_dim; 0 = no rotation */
+  int32_t interleaved;      /* 0 or 1 */
+} kvpop_rope;
+
+/* Norm and rotation of the heads of batch * n_tokens tokens.  q, q_out: rows
+ * with n_q_heads heads; k, k_out: rows with n_kv_heads heads; positions:
+ * device int32 [batch][n_tokens].  dtype KVPOP_DTYPE_*, head_dim 64 or 128.
+ * Runs on the device that q lies on.  batch or n_tokens = 0 is a no-op.
+ * Errors (nothing enqueued): KVPOP_ERR_INVALID_ARG (null or misaligned
+ * pointer, bad stride, q not device memory, eps negative or not finite),
+ * KVPOP_ERR_BAD_SHAPE; KVPOP_ERR_CUDA if the launch fails. */
+int kvpop_qk_norm_rope(int32_t dtype, int32_t head_dim, int32_t n_q_heads, int32_t n_kv_heads,
+                       const kvpop_rope* rope, int32_t batch, int32_t n_tokens, const kvpop_rows* q,
+                       const kvpop_rows* k, const int32_t* positions, const kvpop_rows* q_out,
+                       const kvpop_rows* k_out, void* stream);
+
+/* How a paged cache holds its rows (kvpop_paged_config.cache_format). */
+#define KVPOP_CACHE_NATIVE 0   /* in dtype */
+#define KVPOP_CACHE_E4M3 1     /* 8 bits (e4m3) with one fp32 scale per key row and per value row; dtype bf16 only */
+
+typedef struct kvpop_paged_config {
+  int32_t n_layers;      /* >= 1 */
+  int32_t n_q_heads;     /* a multiple of n_kv_heads, at most 16 per KV head */
+  int32_t n_kv_heads;    /* 1..1024 */
+  int32_t head_dim;      /* 64 or 128 */
+  int32_t page_size;     /* tokens of a page: 16, 32, 64, 128 or 256 */
+  int32_t n_pages;       /* pages of each layer; n_pages * page_size < 2^31 */
+  int32_t max_batch;     /* most sequences of one kvpop_paged_attend: 1..1024 */
+  int32_t dtype;         /* of q, k, v and outputs: KVPOP_DTYPE_* */
+  int32_t cache_format;  /* KVPOP_CACHE_* */
+} kvpop_paged_config;
+
+typedef struct kvpop_paged_handle kvpop_paged_handle;
+
+/* Offsets (bytes, from dev_mem) of a paged cache's arrays; layer l's start at
+ * offset + l * *_layer_stride.  A caller may read and write them directly,
+ * ordered with the calls that use them. */
+typedef struct kvpop_paged_layout_info {
+  size_t pages_offset, pages_layer_stride;     /* [n_pages][n_kv_heads][2 (key, value)][page_size][head_dim] held elements */
+  size_t scales_offset, scales_layer_stride;   /* fp32 [n_pages][n_kv_heads][2][page_size]; 0, 0 for KVPOP_CACHE_NATIVE */
+} kvpop_paged_layout_info;
+
+/* Device bytes of a paged cache.  Host only.  Errors: KVPOP_ERR_INVALID_ARG
+ * (null argument; unknown dtype or cache_format; e4m3 with fp32),
+ * KVPOP_ERR_BAD_SHAPE. */
+int kvpop_paged_bytes(const kvpop_paged_config* cfg, size_t* bytes);
+
+/* Binds a caller-allocated buffer (>= kvpop_paged_bytes, 256-byte aligned, on
+ * the current device) and clears it to zero, synchronously.  The buffer must
+ * outlive the handle.  Errors as kvpop_create. */
+int kvpop_paged_create(const kvpop_paged_config* cfg, void* dev_mem, size_t bytes, kvpop_paged_handle** out);
+
+/* Writes keys and values of batch * n_tokens tokens into layer `layer`.
+ * k, v: rows with n_kv_heads heads.  slots: device int32 [batch][n_tokens];
+ * token t goes to row slots[t] % page_size of page slots[t] / page_size, a
+ * negative slot writes nothing (padding), one past the last page writes
+ * nothing and records KVPOP_DEVERR_BAD_INDEX.  With KVPOP_CACHE_E4M3, per row:
+ *   scale = max |x| * c,  c = fp32(1 / 448),  held = e4m3(x / scale)
+ * (product and quotient rounded to fp32, then to nearest even, at most 448).
+ * A row whose scale is below the smallest normal fp32 number is held as
+ * zeros with scale 0; a row with an infinity or a NaN gets a NaN scale and
+ * reads back as NaN.  Two tokens of one call must not share a slot (which
+ * one's bytes stay would be undefined, element by element; other rows are
+ * not touched).  n_tokens = 0 is a no-op.  Errors (nothing enqueued):
+ * KVPOP_ERR_INVALID_ARG, KVPOP_ERR_BAD_SHAPE; KVPOP_ERR_CUDA. */
+int kvpop_paged_append(kvpop_paged_handle* h, int32_t layer, const kvpop_rows* k, const kvpop_rows* v,
+                       const int32_t* slots, int32_t batch, int32_t n_tokens, void* stream);
+
+/* kvpop_qk_norm_rope and kvpop_paged_append in one launch: queries go to
+ * q_out, keys are normalised, turned and written to their slots without being
+ * rounded in between (with KVPOP_CACHE_E4M3 they are quantised from fp32),
+ * values are written as they are.  Queries of padding tokens (negative slots)
+ * are still written.  Arguments and errors as those two calls. */
+int kvpop_paged_append_qkv(kvpop_paged_handle* h, int32_t layer, const kvpop_rope* rope, const kvpop_rows* q,
+                           const kvpop_rows* k, const kvpop_rows* v, const int32_t* positions,
+                           const int32_t* slots, const kvpop_rows* q_out, int32_t batch, int32_t n_tokens,
+                           void* stream);
+
+/* Reads `batch` sequences back: token i < lens[b] of sequence b, held in row
+ * i % page_size of page page_table[b * table_stride + i / page_size], goes to
+ * row (b, i) of k_out and v_out (rows with n_kv_heads heads and n_tokens
+ * tokens per sequence), in dtype.  Rows at and past lens[b] are left as they
+ * were.  page_table: device int32, table_width entries per sequence; lens:
+ * device int32 [batch].  Sequences may share pages.  A length that is
+ * negative or past n_tokens or table_width * page_size, or a page outside
+ * [0, n_pages), records KVPOP_DEVERR_BAD_INDEX: the length is cut to the
+ * range, and the rows of such a page are left as they were.  Errors (nothing
+ * enqueued): KVPOP_ERR_INVALID_ARG, KVPOP_ERR_BAD_SHAPE; KVPOP_ERR_CUDA. */
+int kvpop_paged_gather(kvpop_paged_handle* h, int32_t layer, const int32_t* page_table, int64_t table_stride,
+                       int32_t table_width, const int32_t* lens, int32_t batch, int32_t n_tokens,
+                       const kvpop_rows* k_out, const kvpop_rows* v_out, void* stream);
+
+/* Options of kvpop_paged_attend; a null pointer means all zero. */
+typedef struct kvpop_attend_options {
+  float scale;      /* > 0, or 0 = 1 / sqrt(head_dim) */
+  float softcap;    /* > 0: scores become softcap * tanh(score / softcap); 0 = none */
+  int32_t window;   /* > 0: the last `window` tokens of each sequence alone are attended; 0 = all */
+} kvpop_attend_options;
+
+/* Attention of one new token per sequence over its pages:
+ *   s_j = scale q . k_j (capped),  out = sum_j softmax(s)_j v_j
+ * over the tokens j < lens[b] (the last `window` of them), fp32 accumulation,
+ * one launch; the work of all sequences is split evenly over the GPU along
+ * the cache's length and joined in a fixed order, so equal calls give equal
+ * bits.  q, out: device [batch][n_q_heads][head_dim] in dtype, 16-byte
+ * aligned; lse: device fp32 [batch][n_q_heads] receiving log sum_j e^(s_j),
+ * or NULL.  page_table, lens as kvpop_paged_gather; 0 <= batch <= max_batch.
+ * A sequence with no token gets out = 0, lse = -inf.  Infinities and NaN in
+ * tokens that are not attended do not reach the result; a NaN or +inf score
+ * gives NaN.  A length that is negative or past table_width * page_size
+ * (cut to the range) or a page outside [0, n_pages) (its tokens are left
+ * out) records KVPOP_DEVERR_BAD_INDEX.  Calls on one handle share its
+ * scratch: order them on one stream or by events, replays of captured graphs
+ * among them.  Errors (nothing enqueued): KVPOP_ERR_INVALID_ARG,
+ * KVPOP_ERR_BAD_SHAPE; KVPOP_ERR_CUDA. */
+int kvpop_paged_attend(kvpop_paged_handle* h, int32_t layer, const void* q, const int32_t* page_table,
+                       int64_t table_stride, int32_t table_width, const int32_t* lens, int32_t batch,
+                       const kvpop_attend_options* options, void* out, float* lse, void* stream);
+
+/* Layout, errors and release of a paged handle, as the kvpop_ calls of the
+ * same names. */
+int kvpop_paged_get_layout(const kvpop_paged_handle* h, kvpop_paged_layout_info* out);
+int kvpop_paged_get_error(kvpop_paged_handle* h, int32_t* device_bits);
+int kvpop_paged_clear_error(kvpop_paged_handle* h, void* stream);
+int kvpop_paged_destroy(kvpop_paged_handle* h);
+
 /* Static description of a status code (diagnostic; no passage defines it). */
 const char* kvpop_status_string(int status);
 

@@ -1,0 +1,184 @@
+"""Paged cache and heads: the oracle's own checks, and every refusal that needs no GPU."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import fixed_budget_kv_kvpop_b200 as kp
+from oracle import paged_oracle as po
+
+CFG = dict(n_layers=2, n_q_heads=8, n_kv_heads=2, head_dim=128, page_size=16, n_pages=10, max_batch=4)
+
+
+def _bytes(**kw):
+    cfg = kp.make_paged_config(**{**CFG, **kw})
+    n = ctypes.c_size_t(0)
+    return kp.lib.kvpop_paged_bytes(ctypes.byref(cfg), ctypes.byref(n)), n.value
+
+
+# ---- oracle ----
+
+def test_e4m3_rounding_matches_torch():
+    x = np.concatenate([np.linspace(-460, 460, 40001), np.random.default_rng(0).normal(size=20000) * 0.02,
+                        po.e4m3_grid(), -po.e4m3_grid()])
+    x = x.astype(np.float32)
+    got = po.round_e4m3(x.astype(np.float64))
+    want = torch.from_numpy(x).clamp(-448, 448).to(torch.float8_e4m3fn).double().numpy()
+    np.testing.assert_array_equal(got, want)
+
+
+def test_held_rows():
+    """The largest magnitude of a row stands for 448, half of it for 224; tiny and zero rows are zeros; bad rows are NaN."""
+    x = np.array([[1.0, -0.5, 0.25, 0.0], [0, 0, 0, 0], [1e-37, 0, 0, 0], [np.inf, 1, 1, 1], [1, np.nan, 1, 1]])
+    h, s = po.hold_e4m3(x)
+    np.testing.assert_array_equal(h[0], [448, -224, 112, 0])
+    assert s[0] == np.float32(1.0) / np.float32(448)
+    assert (h[1] == 0).all() and s[1] == 0 and (h[2] == 0).all() and s[2] == 0
+    assert np.isnan(h[3:]).all() and np.isnan(s[3:]).all()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_heads_keep_norm_and_relative_angle(interleaved):
+    """A rotation keeps lengths, and q . k depends on the distance of the two positions alone."""
+    rng = np.random.default_rng(1)
+    x = rng.normal(size=(6, 2, 64))
+    f = 1e4 ** (-np.arange(0, 64, 2) / 64)
+    y = po.heads(x, None, 0.0, np.arange(6) * 1000, f, interleaved=interleaved)
+    np.testing.assert_allclose(np.linalg.norm(y, axis=-1), np.linalg.norm(x, axis=-1), rtol=1e-12)
+    q, k = rng.normal(size=(1, 1, 64)), rng.normal(size=(1, 1, 64))
+    dots = [float((po.heads(q, None, 0, [p + 5], f, interleaved=interleaved)
+                   * po.heads(k, None, 0, [p], f, interleaved=interleaved)).sum()) for p in (0, 77, 123456)]
+    np.testing.assert_allclose(dots, dots[0], rtol=1e-8)
+
+
+def test_heads_hand_example():
+    """Weights 2, one pair turned by a right angle: (a, b) -> (-b, a); the rest stays."""
+    x = np.array([[[3.0, 0, 0, 0, 4.0, 0, 0, 0] + [0.0] * 8]])
+    y = po.heads(x, np.full(16, 2.0), 0.0, [1], [np.pi / 2, 0, 0, 0])
+    rms = 5.0 / 4.0
+    np.testing.assert_allclose(y[0, 0, :8], np.array([-4.0, 0, 0, 0, 3.0, 0, 0, 0]) * 2 / rms, atol=1e-14)
+
+
+def test_attend_matches_softmax():
+    rng = np.random.default_rng(2)
+    q, k, v = rng.normal(size=(6, 64)), rng.normal(size=(9, 2, 64)), rng.normal(size=(9, 2, 64))
+    out, lse = po.attend(q, k, v)
+    for h in range(6):
+        s = torch.from_numpy(k[:, h // 3] @ q[h]) / 8.0
+        np.testing.assert_allclose(out[h], (torch.softmax(s, 0) @ torch.from_numpy(v[:, h // 3])).numpy(), rtol=1e-12)
+        np.testing.assert_allclose(lse[h], torch.logsumexp(s, 0).item(), rtol=1e-12)
+    wide, _ = po.attend(q, k, v, window=9)
+    np.testing.assert_array_equal(wide, out)
+    one, l1 = po.attend(q, k, v, window=1)
+    np.testing.assert_allclose(one[0], v[-1, 0], rtol=1e-12)
+    none, l0 = po.attend(q, k[:0], v[:0])
+    assert (none == 0).all() and (l0 == -np.inf).all()
+
+
+# ---- refusals ----
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n_layers=0), kp.KVPOP_ERR_BAD_SHAPE), (dict(n_pages=0), kp.KVPOP_ERR_BAD_SHAPE),
+    (dict(max_batch=0), kp.KVPOP_ERR_BAD_SHAPE), (dict(max_batch=1025), kp.KVPOP_ERR_BAD_SHAPE),
+    (dict(n_q_heads=7), kp.KVPOP_ERR_BAD_SHAPE), (dict(n_q_heads=34), kp.KVPOP_ERR_BAD_SHAPE),   # 17 heads per KV head
+    (dict(head_dim=96), kp.KVPOP_ERR_BAD_SHAPE), (dict(page_size=8), kp.KVPOP_ERR_BAD_SHAPE),
+    (dict(page_size=48), kp.KVPOP_ERR_BAD_SHAPE), (dict(page_size=512), kp.KVPOP_ERR_BAD_SHAPE),
+    (dict(n_pages=1 << 27), kp.KVPOP_ERR_BAD_SHAPE),                                             # 2^31 rows
+    (dict(n_kv_heads=1025, n_q_heads=1025), kp.KVPOP_ERR_BAD_SHAPE),
+    (dict(dtype="f32", cache="e4m3"), kp.KVPOP_ERR_INVALID_ARG),
+])
+def test_bad_paged_configs_are_refused(kw, code):
+    assert _bytes(**kw)[0] == code
+
+
+def test_paged_bytes_count_rows_and_scales():
+    rows = 2 * 10 * 2 * 2 * 16        # layers, pages, heads, key and value, page_size
+    st, n = _bytes()
+    assert st == kp.KVPOP_OK and n >= rows * 256
+    st, n8 = _bytes(cache="e4m3")
+    assert st == kp.KVPOP_OK and rows * (128 + 4) <= n8 < n
+    st, big = _bytes(n_layers=80, n_pages=1 << 20, page_size=256, n_kv_heads=64, n_q_heads=64)
+    assert st == kp.KVPOP_OK and big > 80 * (1 << 20) * 256 * 64 * 2 * 256
+
+
+def test_unknown_codes_are_refused():
+    cfg = kp.make_paged_config(**CFG)
+    n = ctypes.c_size_t(0)
+    cfg.dtype = 7
+    assert kp.lib.kvpop_paged_bytes(ctypes.byref(cfg), ctypes.byref(n)) == kp.KVPOP_ERR_INVALID_ARG
+    cfg.dtype, cfg.cache_format = kp.KVPOP_DTYPE_BF16, 2
+    assert kp.lib.kvpop_paged_bytes(ctypes.byref(cfg), ctypes.byref(n)) == kp.KVPOP_ERR_INVALID_ARG
+    with pytest.raises(ValueError, match="cache format"):
+        kp.make_paged_config(**CFG, cache="int8")
+
+
+def test_null_handles_and_host_memory_are_refused():
+    bad = kp.KVPOP_ERR_INVALID_ARG
+    L = kp.lib
+    assert L.kvpop_paged_bytes(None, None) == bad
+    assert L.kvpop_paged_append(None, 0, None, None, None, 1, 1, None) == bad
+    assert L.kvpop_paged_append_qkv(None, 0, None, None, None, None, None, None, None, 1, 1, None) == bad
+    assert L.kvpop_paged_gather(None, 0, None, 1, 1, None, 1, 1, None, None, None) == bad
+    assert L.kvpop_paged_attend(None, 0, None, None, 1, 1, None, 1, None, None, None, None) == bad
+    assert L.kvpop_paged_get_layout(None, None) == bad
+    assert L.kvpop_paged_get_error(None, None) == bad
+    assert L.kvpop_paged_clear_error(None, None) == bad
+    assert L.kvpop_paged_destroy(None) == bad
+    cfg = kp.make_paged_config(**CFG)
+    n = kp.paged_bytes(cfg)
+    buf = ctypes.create_string_buffer(n + 256)
+    h = ctypes.c_void_p()
+    addr = (ctypes.addressof(buf) + 255) // 256 * 256
+    assert L.kvpop_paged_create(ctypes.byref(cfg), ctypes.c_void_p(addr), n, ctypes.byref(h)) == bad
+    assert not h.value
+    assert L.kvpop_paged_create(ctypes.byref(cfg), None, n, ctypes.byref(h)) == bad
+
+
+def _heads_call(dtype=kp.KVPOP_DTYPE_BF16, d=128, hq=4, hkv=2, rope=None, batch=1, n=1, addr=None, strides=(0, 0, 128),
+                pos=64):
+    """kvpop_qk_norm_rope on host memory: every argument but that is in order."""
+    buf = ctypes.create_string_buffer(8192)
+    base = (ctypes.addressof(buf) + 255) // 256 * 256
+    r = kp._pack_rows(base if addr is None else addr, *strides)
+    rope = kp._pack_rope(0, 0, base, 1e-6, 1.0, 128, 0) if rope is None else rope
+    return kp.lib.kvpop_qk_norm_rope(dtype, d, hq, hkv, rope, batch, n, r, r, base + pos if pos else None, r, r, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=5), kp.KVPOP_ERR_INVALID_ARG), (dict(d=80), kp.KVPOP_ERR_BAD_SHAPE),
+    (dict(hq=0), kp.KVPOP_ERR_BAD_SHAPE), (dict(hkv=2000), kp.KVPOP_ERR_BAD_SHAPE),
+    (dict(batch=-1), kp.KVPOP_ERR_INVALID_ARG), (dict(n=-1), kp.KVPOP_ERR_INVALID_ARG),
+    (dict(rope=kp._pack_rope(0, 0, 4096, 1e-6, 1.0, 132, 0)), kp.KVPOP_ERR_BAD_SHAPE),    # rot_dim past head_dim
+    (dict(rope=kp._pack_rope(0, 0, 4096, 1e-6, 1.0, 20, 0)), kp.KVPOP_ERR_BAD_SHAPE),     # not a multiple of 8
+    (dict(rope=kp._pack_rope(0, 0, 0, 1e-6, 1.0, 64, 0)), kp.KVPOP_ERR_INVALID_ARG),      # no frequencies
+    (dict(rope=kp._pack_rope(8, 0, 4096, 1e-6, 1.0, 64, 0)), kp.KVPOP_ERR_INVALID_ARG),   # misaligned weights
+    (dict(rope=kp._pack_rope(0, 0, 4096, -1.0, 1.0, 64, 0)), kp.KVPOP_ERR_INVALID_ARG),
+    (dict(rope=kp._pack_rope(0, 0, 4096, float("nan"), 1.0, 64, 0)), kp.KVPOP_ERR_INVALID_ARG),
+    (dict(rope=kp._pack_rope(0, 0, 4096, 1e-6, float("inf"), 64, 0)), kp.KVPOP_ERR_INVALID_ARG),
+    (dict(rope=kp._pack_rope(0, 0, 4096, 1e-6, 1.0, 64, 2)), kp.KVPOP_ERR_INVALID_ARG),
+    (dict(addr=0), kp.KVPOP_ERR_INVALID_ARG), (dict(addr=4104), kp.KVPOP_ERR_INVALID_ARG),
+    (dict(strides=(0, 0, -128)), kp.KVPOP_ERR_INVALID_ARG), (dict(strides=(0, 0, 129)), kp.KVPOP_ERR_INVALID_ARG),
+    (dict(strides=(0, 0, 0)), kp.KVPOP_ERR_INVALID_ARG),                                   # an output expanded over heads
+    (dict(pos=0), kp.KVPOP_ERR_INVALID_ARG), (dict(pos=66), kp.KVPOP_ERR_INVALID_ARG),
+    (dict(), kp.KVPOP_ERR_INVALID_ARG),                                                    # host memory
+    (dict(batch=0), kp.KVPOP_OK), (dict(n=0), kp.KVPOP_OK),
+])
+def test_heads_refusals(kw, code):
+    assert _heads_call(**kw) == code
+
+
+def test_binding_refuses_host_tensors_and_bad_rope():
+    f = torch.zeros(32, dtype=torch.float64)
+    with pytest.raises(ValueError, match="cuda"):
+        kp.make_rope(f)
+    q = torch.zeros(1, 1, 4, 64)
+    with pytest.raises(ValueError, match="cuda"):
+        kp.qk_norm_rope(None, q, q, torch.zeros(1, 1, dtype=torch.int32), q, q)
+    dev = torch.device("cuda", 0)
+    with pytest.raises(ValueError, match="expected the cuda device"):
+        kp._rows(q, "q", q.shape, torch.float32, dev)
+    with pytest.raises(ValueError, match="torch.Tensor"):
+        kp._rows([1.0], "q", (1,), torch.float32, dev)
+    with pytest.raises(ValueError, match="int32"):
+        kp._ints(torch.zeros(3, dtype=torch.int64), "slots", (3,), dev)
