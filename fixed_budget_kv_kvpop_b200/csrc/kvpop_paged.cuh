@@ -14,6 +14,7 @@
 namespace kvpop {
 
 constexpr int kMaxGroup = 16;      // query heads per KV head that the attention is built for
+constexpr int kAttendRanges = 512; // most CTAs of one attention launch
 
 // What a kernel needs of one layer's pages.
 struct PagedLayer {
@@ -77,6 +78,15 @@ enum HeadsMode : int { HEADS_DENSE = 0, HEADS_APPEND = 1, HEADS_STEP = 2 };
 // All return 0, -1 (a CUDA call failed) or -2 (shape not built).
 int launch_heads(const HeadsArgs& a, int dtype, int d, int mode, int num_sms, cudaStream_t st);
 int launch_gather(const GatherArgs& a, int dtype, int d, cudaStream_t st);
-int launch_attend(const AttendArgs& a, int dtype, int d, int num_sms, cudaStream_t st);
+int launch_attend(const CUtensorMap& map, const AttendArgs& a, void* scratch, int dtype, int d, int num_sms,
+                  cudaStream_t st);
+// Scratch of the attention: partials of kAttendRanges ranges and one arrival
+// ticket per unit.  Must be zero before the first launch; each launch leaves
+// the tickets zero.
+size_t attend_scratch_bytes(int G, int d, int units);
+// Tensor map over one layer's pages for the attention's copies of 16 keys and values.
+int make_attend_map(CUtensorMap* map, void* pages, int dtype, int d, bool e8, int page_size, int64_t page_heads);
+// Sets what the attention kernel of a handle needs on the current device.
+int prepare_attend(int dtype, int d, bool e8, int G);
 
 }  // namespace kvpop

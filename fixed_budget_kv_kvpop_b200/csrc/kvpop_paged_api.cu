@@ -16,7 +16,7 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 int element_size(int dtype) { return dtype == KVPOP_DTYPE_F32 ? 4 : 2; }
 
 struct PagedLayout {
-  size_t pages_off, pages_stride, scales_off, scales_stride, err_off, total;
+  size_t pages_off, pages_stride, scales_off, scales_stride, scratch_off, err_off, total;
 };
 
 int validate(const kvpop_paged_config* c) {
@@ -31,6 +31,7 @@ int validate(const kvpop_paged_config* c) {
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128 && c->page_size != 256)
     return KVPOP_ERR_BAD_SHAPE;
   if (static_cast<int64_t>(c->n_pages) * c->page_size > 2147483647) return KVPOP_ERR_BAD_SHAPE;
+  if (static_cast<int64_t>(c->n_pages) * c->n_kv_heads > 2147483647) return KVPOP_ERR_BAD_SHAPE;   // a copy's coordinate
   // the bytes of all layers stay far below 2^63
   const double bytes = static_cast<double>(c->n_layers) * c->n_pages * c->page_size * c->n_kv_heads * 2.0 *
                        c->head_dim * 4.0;
@@ -47,6 +48,8 @@ PagedLayout make_layout(const kvpop_paged_config* c) {
   L.pages_off = off; off += c->n_layers * L.pages_stride;
   L.scales_stride = e8 ? align256(rows * 4) : 0;
   L.scales_off = e8 ? off : 0; off += c->n_layers * L.scales_stride;
+  L.scratch_off = off;
+  off += align256(attend_scratch_bytes(c->n_q_heads / c->n_kv_heads, c->head_dim, c->max_batch * c->n_kv_heads));
   L.err_off = off; off += 256;
   L.total = off;
   return L;
@@ -123,6 +126,8 @@ struct kvpop_paged_handle {
   PagedLayout lay;
   uint8_t* mem;
   int device, num_sms, page_shift;
+  CUtensorMap* maps = nullptr;   // per layer
+  ~kvpop_paged_handle() { delete[] maps; }
 };
 
 namespace {
@@ -210,7 +215,13 @@ int kvpop_paged_create(const kvpop_paged_config* cfg, void* dev_mem, size_t byte
   h->device = dev;
   h->num_sms = sms;
   for (h->page_shift = 4; (1 << h->page_shift) < cfg->page_size;) ++h->page_shift;
-  if (cudaMemset(h->mem, 0, L.total) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  const bool e8 = cfg->cache_format == KVPOP_CACHE_E4M3;
+  h->maps = new (std::nothrow) CUtensorMap[cfg->n_layers];
+  bool ok = h->maps != nullptr && prepare_attend(cfg->dtype, cfg->head_dim, e8, cfg->n_q_heads / cfg->n_kv_heads) == 0;
+  for (int l = 0; ok && l < cfg->n_layers; ++l)
+    ok = make_attend_map(&h->maps[l], h->mem + L.pages_off + l * L.pages_stride, cfg->dtype, cfg->head_dim, e8,
+                         cfg->page_size, static_cast<int64_t>(cfg->n_pages) * cfg->n_kv_heads) == 0;
+  if (!ok || cudaMemset(h->mem, 0, L.total) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     delete h;
     return KVPOP_ERR_CUDA;
   }
@@ -296,6 +307,7 @@ int kvpop_paged_attend(kvpop_paged_handle* h, int32_t layer, const void* q, cons
   if (batch == 0) return KVPOP_OK;
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return KVPOP_ERR_INVALID_ARG;
   if (!tables_ok(page_table, table_stride, table_width, lens, batch)) return KVPOP_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(table_width) * c.page_size > (1 << 30)) return KVPOP_ERR_BAD_SHAPE;
   AttendArgs a{};
   a.pg = paged_layer(h, layer);
   a.q = q; a.table = page_table; a.lens = lens; a.table_stride = table_stride;
@@ -306,7 +318,8 @@ int kvpop_paged_attend(kvpop_paged_handle* h, int32_t layer, const void* q, cons
   a.window = o.window;
   DeviceScope scope(h->device);
   if (!scope.ok()) return KVPOP_ERR_CUDA;
-  return status_of(launch_attend(a, c.dtype, c.head_dim, h->num_sms, static_cast<cudaStream_t>(stream)));
+  return status_of(launch_attend(h->maps[layer], a, h->mem + h->lay.scratch_off, c.dtype, c.head_dim,
+                                 h->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 int kvpop_paged_get_layout(const kvpop_paged_handle* h, kvpop_paged_layout_info* o) {

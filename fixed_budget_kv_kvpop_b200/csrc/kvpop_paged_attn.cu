@@ -1,41 +1,674 @@
-// Attention of one new token per sequence over its pages.
+// Attention of one new token per sequence over its pages, in one launch.
 //
 //   s_j = scale q . k_j  (then cap tanh(s_j / cap)),  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m)
 //
-// Simple form: one block per (sequence, query head); each warp walks every
-// fourth key with a running maximum and sum, and the warps are joined at the end.
+// Work split.  A unit is one (sequence, KV head); its keys are cut into blocks
+// of KB.  The blocks of all units form one sequence, cut into equal contiguous
+// ranges, one per CTA, whatever the lengths of the sequences are; each CTA finds
+// its range from the lengths on the device.  A unit that lies in several ranges
+// leaves one partial (accumulator, running maximum, sum) per CTA, and the CTA
+// that arrives last joins them in the order of the ranges, so results do not
+// depend on who is last.
+// Inside a CTA each warp has a ring of stages of its own: it copies block after
+// block into it by tensor copies (one instruction per 16 keys and values) and
+// computes on the oldest.  Warps meet once per unit, to join their sums.
 #include "kvpop_paged.cuh"
 
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include <cudaTypedefs.h>
 
 namespace kvpop {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int NW = 4;                    // warps per CTA
+constexpr int kCtasPerSm = 2;
+constexpr int kUnitBlocks = 16;          // units of at most this many blocks are not split
+constexpr int kMinShare = 8;             // blocks of a range at least
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kRaise = 8.f;            // a running maximum moves when a score passes it by this (in powers of two)
 
-template <typename T, int D, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32) attend_simple_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float sm_acc[kWarps][D], sm_m[kWarps], sm_l[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int hq = blockIdx.x, b = blockIdx.y, h = hq / a.G;
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int x, int y, int z, int k, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+      :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(k), "r"(w),
+         "r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16_16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+               "{%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Four e4m3 bytes -> bytes 0, 2 and bytes 1, 3 as bf16 pairs, exactly: sign,
+// exponent and fraction are moved to their bf16 places, which gives the value
+// times 2^-120 (subnormals included), and one product puts that right.
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t x, uint32_t& even, uint32_t& odd) {
+  constexpr uint32_t k2p120 = 0x7b807b80u;
+  even = mul_bf16x2(((x << 4) & 0x07f007f0u) | ((x << 8) & 0x80008000u), k2p120);
+  odd = mul_bf16x2(((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), k2p120);
+}
+// Two e4m3 bytes -> f16 pair.
+__device__ __forceinline__ uint32_t e4m3_to_f16(uint16_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+  return r;
+}
+
+// Attended tokens [lo, n) of sequence b.  Lengths outside the table are cut.
+struct Span {
+  int lo, n;
+};
+__device__ __forceinline__ Span span_of(const AttendArgs& a, int b) {
   int n = a.lens[b];
   const int64_t cap = static_cast<int64_t>(a.width) << a.pg.page_shift;
-  if (n < 0 || n > cap) {
-    if (threadIdx.x == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
-    n = n < 0 ? 0 : static_cast<int>(cap);
+  n = n < 0 ? 0 : n > cap ? static_cast<int>(cap) : n;
+  return Span{a.window > 0 && n > a.window ? n - a.window : 0, n};
+}
+
+// Walks the segments of a CTA: runs of blocks of one unit, in order.
+template <int KB>
+struct Walk {
+  int b, h;          // unit
+  int lo, n;         // its attended tokens
+  int j, jend;       // blocks [j, jend) of the segment; block x holds tokens x KB .. x KB + KB - 1
+  int jlo, jhi;      // the unit's blocks
+  int64_t left;      // blocks of the CTA's range from this segment on
+  int64_t index;     // position of the segment's first block among all blocks
+
+  __device__ __forceinline__ void unit(const AttendArgs& a) {
+    const Span s = span_of(a, b);
+    lo = s.lo; n = s.n;
+    jlo = lo / KB;
+    jhi = (n + KB - 1) / KB;
   }
-  const int lo = a.window > 0 && n > a.window ? n - a.window : 0;
+  __device__ __forceinline__ void cut() { jend = static_cast<int>(min(static_cast<int64_t>(jhi), j + left)); }
+  // To the next segment; false at the end of the range.
+  __device__ __forceinline__ bool next(const AttendArgs& a, int unit_step) {
+    if (unit_step > 0) {            // whole units, unit_step apart
+      do {
+        const int u = b * a.pg.Hkv + h + unit_step;
+        if (u >= a.batch * a.pg.Hkv) return false;
+        b = u / a.pg.Hkv; h = u % a.pg.Hkv;
+        unit(a);
+      } while (jhi == jlo);
+      j = jlo; jend = jhi;
+      return true;
+    }
+    left -= jend - j;
+    index += jend - j;
+    if (left <= 0) return false;
+    if (++h == a.pg.Hkv) {
+      h = 0;
+      do { ++b; unit(a); } while (jhi == jlo);   // blocks are left, so a unit that has some follows
+    }
+    j = jlo;
+    cut();
+    return true;
+  }
+};
+
+template <int D, bool E4M3, int GP>
+struct Geo {
+  static constexpr int ES = E4M3 ? 1 : 2;
+  static constexpr int SUB = 2 * 16 * D * ES;                // bytes of 16 keys and values
+  static constexpr int NSUB = 8192 / SUB;
+  static constexpr int KB = 16 * NSUB;                       // keys of a block (one stage)
+  static constexpr int ROWB = D * ES < 128 ? D * ES : 128;   // bytes of a row in one box
+  static constexpr int HALVES = D * ES / ROWB;
+  static constexpr int SCALE = E4M3 ? NSUB * 128 : 0;        // bytes of scales of a stage
+  static constexpr int MERGE = NW * GP * (D + 4) * 4;
+  static constexpr int CTA = (227 * 1024 - kCtasPerSm * 1024) / kCtasPerSm;
+  static constexpr int NST0 = (CTA - 1024 - MERGE - 512) / (NW * (8192 + SCALE + 16));
+  static constexpr int NST = NST0 > 8 ? 8 : NST0;
+  static constexpr int SMEM = 1024 + NW * NST * (8192 + SCALE + 16) + MERGE + 256;
+};
+
+struct AttendScratch {
+  float* acc;        // [ranges][2][G][D]
+  float* ml;         // [ranges][2][G][4]: running maximum, sum, whether any key was seen
+  int32_t* ticket;   // [units], zero between launches
+};
+
+template <int D, bool E4M3, int GP>
+__global__ void __launch_bounds__(NW * 32, kCtasPerSm)
+attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendArgs a, const AttendScratch sc) {
+  using G_ = Geo<D, E4M3, GP>;
+  constexpr int KB = G_::KB, NSUB = G_::NSUB, NST = G_::NST;
+  constexpr int R = GP == 16 ? 2 : 1;      // query rows per lane
+  constexpr int KS = D / 16;               // 16-wide steps over the head
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + warp * NST * 8192;
+  uint8_t* sring = smem + NW * NST * 8192 + warp * NST * G_::SCALE;
+  float* macc = reinterpret_cast<float*>(smem + NW * NST * (8192 + G_::SCALE));   // [NW][GP][D]
+  float* mml = macc + NW * GP * D;                                                // [NW][GP][4]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(mml + NW * GP * 4) + warp * NST;
+  int32_t* live = reinterpret_cast<int32_t*>(reinterpret_cast<uint64_t*>(mml + NW * GP * 4) + NW * NST) + warp * NST;
+  __shared__ int last_flag;
+
+  if (lane == 0) {
+    for (int s = 0; s < NST; ++s) mbar_init(&bars[s], 1);
+    mbar_fence_init();
+  }
+  __syncwarp();
+
+  // ---- this CTA's range ----
+  const int Hkv = a.pg.Hkv, G = a.G;
+  int64_t total = 0;
+  int longest = 0;
+  bool bad_len = false;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int b = b0 + lane;
+    int nb = 0;
+    if (b < a.batch) {
+      const Span s = span_of(a, b);
+      nb = (s.n + KB - 1) / KB - s.lo / KB;
+      bad_len |= a.lens[b] != s.n;
+    }
+    total += nb;
+    longest = max(longest, nb);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  }
+  if (bad_len && blockIdx.x == 0 && warp == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
+  total *= Hkv;
+  const int n_cta = gridDim.x;
+  const bool whole = longest <= kUnitBlocks;
+  int64_t share = (total + n_cta - 1) / n_cta;
+  if (share < kMinShare) share = kMinShare;
+  const int unit_step = whole ? n_cta : 0;
+
+  // sequences without a token
+  for (int b = blockIdx.x; b < a.batch; b += n_cta) {
+    const Span s = span_of(a, b);
+    if (s.n > 0) continue;
+    for (int i = threadIdx.x; i < a.Hq * D; i += NW * 32)
+      static_cast<__nv_bfloat16*>(a.out)[static_cast<int64_t>(b) * a.Hq * D + i] = __float2bfloat16_rn(0.f);
+    if (a.lse)
+      for (int i = threadIdx.x; i < a.Hq; i += NW * 32) a.lse[static_cast<int64_t>(b) * a.Hq + i] = -INFINITY;
+  }
+
+  Walk<KB> w;
+  bool more = true;
+  if (whole) {
+    w.b = 0; w.h = static_cast<int>(blockIdx.x) - n_cta;
+    // unit blockIdx.x: one step from the unit before it
+    w.b = 0;
+    more = w.next(a, n_cta);
+    w.index = 0; w.left = 0;
+  } else {
+    const int64_t beg = share * blockIdx.x;
+    more = beg < total;
+    if (more) {
+      // the sequence that block `beg` lies in
+      int64_t before = 0;
+      int b0 = 0;
+      for (;; b0 += 32) {
+        const int b = b0 + lane;
+        int64_t nb = 0;
+        if (b < a.batch) {
+          const Span s = span_of(a, b);
+          nb = static_cast<int64_t>((s.n + KB - 1) / KB - s.lo / KB) * Hkv;
+        }
+        int64_t incl = nb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, before + incl > beg);
+        if (past) {
+          const int i = __ffs(past) - 1;
+          w.b = b0 + i;
+          before += __shfl_sync(0xffffffffu, incl - nb, i);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      w.unit(a);
+      const int per = w.jhi - w.jlo;
+      w.h = static_cast<int>((beg - before) / per);
+      w.j = w.jlo + static_cast<int>((beg - before) % per);
+      w.left = min(share, total - beg);
+      w.index = beg;
+      w.cut();
+    }
+  }
+  if (!more) return;     // the whole CTA
+
+  // ---- the producer side of this warp: a second walk, NST blocks ahead ----
+  Walk<KB> p = w;
+  bool p_more = true;
+  int pj = 0, seq_p = 0, page_next = -1;
+  bool dead = false;     // a wait ran out: nothing more is copied or computed
+  // first own block of a segment: blocks go to the warps in turn
+  auto first_own = [&](const Walk<KB>& x) { return x.j + static_cast<int>((warp - x.index) & (NW - 1)); };
+  auto settle = [&]() {  // moves p to a segment that has a block for this warp
+    while (p_more && pj >= p.jend) {
+      p_more = p.next(a, unit_step);
+      if (p_more) pj = first_own(p);
+    }
+  };
+  auto load_page = [&]() {   // lane i: the page of sub-block i of the next block
+    page_next = -2;
+    if (p_more && lane < NSUB) {
+      const int key = pj * KB + lane * 16;
+      if (key < p.n && key + 16 > p.lo)
+        page_next = a.table[p.b * a.table_stride + (key >> a.pg.page_shift)];
+    }
+  };
+  auto issue = [&]() {
+    if (!p_more || dead) return;
+    const int st = seq_p % NST;
+    const bool want = page_next != -2;
+    const bool ok = want && page_next >= 0 && page_next < a.pg.n_pages;
+    if (want && !ok) set_error(a.pg.err, DEVERR_BAD_INDEX);
+    const unsigned m = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) {
+      live[st] = static_cast<int32_t>(m);
+      mbar_arrive_expect_tx(&bars[st], __popc(m) * (G_::SUB + (E4M3 ? 128 : 0)));
+    }
+    __syncwarp();
+    if (ok) {
+      const int row = (pj * KB + lane * 16) & ((1 << a.pg.page_shift) - 1);
+      const int w5 = page_next * Hkv + p.h;
+      tma_load_5d(ring + st * 8192 + lane * G_::SUB, &map, 0, row, 0, 0, w5, &bars[st]);
+      if (E4M3) {
+        const float* s0 = a.pg.scales + ((static_cast<int64_t>(w5) * 2) << a.pg.page_shift) + row;
+        bulk_g2s(sring + st * G_::SCALE + lane * 128, s0, 64, &bars[st]);
+        bulk_g2s(sring + st * G_::SCALE + lane * 128 + 64, s0 + (1 << a.pg.page_shift), 64, &bars[st]);
+      }
+    }
+    ++seq_p;
+    pj += NW;
+    settle();
+    load_page();
+  };
+  pj = first_own(p);
+  settle();
+  load_page();
+  for (int s = 0; s < NST; ++s) issue();
+
+  // ---- segments ----
+  int seq_c = 0;
+  const float qscale = a.scale * kLog2e;
+  while (more) {
+    // queries as A fragments: row g (and g + 8); up to four heads fill rows 0..3 and again 4..7
+    uint32_t qf[KS][4];
+    float qmul[R];
+    {
+      const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(w.b) * a.Hq + static_cast<int64_t>(w.h) * G) * D;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = GP == 4 ? (g & 3) : g + 8 * r;
+        const bool on = r < R && row < G;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(qb + static_cast<int64_t>(on ? row : 0) * D);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          // bf16: elements 2t, 2t + 1 and 2t + 8, 2t + 9 of a step; 8 bits: 4t .. 4t + 3
+          qf[k][r] = on ? src[k * 8 + (E4M3 ? 2 * t : t)] : 0u;
+          qf[k][r + 2] = on ? src[k * 8 + (E4M3 ? 2 * t + 1 : t + 4)] : 0u;
+        }
+        if (r < R) qmul[r] = qscale;
+        if (E4M3 && r < R) {
+          // to f16, exactly: the row is scaled by a power of two that brings its largest magnitude to [2^13, 2^14)
+          float top = 0.f;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const float2 v = bf2_to_f2(qf[k][r + i]);
+              top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+            }
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+          e = top == 0.f || e > 127 ? 13 : e < -100 ? -100 : e;
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
+          qmul[r] = qscale * __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const float2 v = bf2_to_f2(qf[k][r + i]);
+              const __half2 hv = __floats2half2_rn(v.x * up, v.y * up);
+              qf[k][r + i] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+          }
+        }
+      }
+    }
+    float acc[R][KS][4];
+    float m[R], l[R];
+    bool any = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = -INFINITY; l[r] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[r][k][i] = 0.f;
+    }
+
+    for (int j = first_own(w); j < w.jend; j += NW) {
+      const int st = seq_c % NST;
+      if (!dead && !mbar_wait(&bars[st], (seq_c / NST) & 1)) {
+        if (lane == 0) set_error(a.pg.err, DEVERR_TIMEOUT);
+        dead = true;
+      }
+      dead = __any_sync(0xffffffffu, dead);
+      bool cleared = false;
+      const unsigned have = dead ? 0u : static_cast<unsigned>(live[st]);
+#pragma unroll 1
+      for (int sub = 0; sub < NSUB; ++sub) {
+        if (!((have >> sub) & 1)) continue;
+        any = true;
+        const int key0 = j * KB + sub * 16;
+        uint8_t* kbase = ring + st * 8192 + sub * G_::SUB;
+        const uint32_t ks = smem_u32(kbase), vs = ks + G_::SUB / 2;
+        const bool part = key0 < w.lo || key0 + 16 > w.n;
+        if (part) {
+          // values of tokens that are not attended: whatever they hold, weight zero must give zero
+          const int row = lane >> 1;
+          if (key0 + row < w.lo || key0 + row >= w.n) {
+            constexpr int CH = G_::ROWB / 16;
+#pragma unroll
+            for (int hf = 0; hf < G_::HALVES; ++hf)
+#pragma unroll
+              for (int c = 0; c < CH / 2; ++c)
+                *reinterpret_cast<uint4*>(kbase + G_::SUB / 2 + hf * 16 * G_::ROWB + row * G_::ROWB + ((lane & 1) * (CH / 2) + c) * 16) =
+                    make_uint4(0, 0, 0, 0);
+          }
+          cleared = true;
+          __syncwarp();
+        }
+        // address of 16-byte chunk c of row r
+        auto at = [&](uint32_t base, int r, int c) {
+          if (G_::ROWB == 128) return base + (c >> 3) * (16 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+          return base + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+        };
+        // ---- scores: rows are queries, columns keys 0..7 and 8..15 ----
+        float s[2][2][4];
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[nb][c][i] = 0.f;
+        if constexpr (!E4M3) {
+#pragma unroll
+          for (int k = 0; k < KS / 2; ++k) {
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb) {
+              uint32_t f[4];
+              ldsm_x4(at(ks, nb * 8 + (lane & 7), 4 * k + (lane >> 3)), f);
+              mma_bf16_16816(s[nb][0], qf[2 * k], f[0], f[1]);
+              mma_bf16_16816(s[nb][1], qf[2 * k + 1], f[2], f[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < KS / 4; ++k) {
+#pragma unroll
+            for (int nb = 0; nb < 2; ++nb) {
+              uint32_t f[4];
+              ldsm_x4(at(ks, nb * 8 + (lane & 7), 4 * k + (lane >> 3)), f);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma_f16_16816(s[nb][i & 1], qf[4 * k + i], e4m3_to_f16(static_cast<uint16_t>(f[i])),
+                              e4m3_to_f16(static_cast<uint16_t>(f[i] >> 16)));
+            }
+          }
+        }
+        float2 kf[2], vf[2];
+        if constexpr (E4M3) {
+          const float2* sp = reinterpret_cast<const float2*>(sring + st * G_::SCALE + sub * 128);
+          kf[0] = sp[t]; kf[1] = sp[4 + t]; vf[0] = sp[8 + t]; vf[1] = sp[12 + t];
+        }
+        uint32_t ph[R][2], pl[R][2];     // weights as two bf16 terms
+        float x[R][4];
+        float top[R];
+        bool raise = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float y = s[i >> 1][0][2 * r + (i & 1)] + s[i >> 1][1][2 * r + (i & 1)];
+            if constexpr (E4M3) y *= (i & 1) ? kf[i >> 1].y : kf[i >> 1].x;
+            y *= qmul[r];
+            if (a.softcap > 0.f) y = a.softcap * kLog2e * tanhf(y * (kLn2 / a.softcap));
+            if (part) {
+              const int key = key0 + (i >> 1) * 8 + 2 * t + (i & 1);
+              if (key < w.lo || key >= w.n) y = -INFINITY;
+            }
+            x[r][i] = y;
+          }
+          top[r] = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+          raise |= top[r] > m[r] + kRaise;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            float y = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+            const float m1 = fmaxf(m[r], y);
+            const float c = m[r] == -INFINITY ? 0.f : ex2(m[r] - m1);
+            m[r] = m1;
+            l[r] *= c;
+            // accumulator columns 2t, 2t + 1 belong to rows 2t, 2t + 1
+            const float c0 = __shfl_sync(0xffffffffu, c, 8 * t), c1 = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              acc[r][k][0] *= c0; acc[r][k][1] *= c1;
+              acc[r][k][2] *= c0; acc[r][k][3] *= c1;
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float mu = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb) {
+            float p0 = ex2(x[r][2 * nb] - mu), p1 = ex2(x[r][2 * nb + 1] - mu);
+            l[r] += p0 + p1;
+            if constexpr (E4M3) {
+              // the value's scale goes into its weight; a masked token's scale may be anything
+              p0 = part && x[r][2 * nb] == -INFINITY ? 0.f : p0 * vf[nb].x;
+              p1 = part && x[r][2 * nb + 1] == -INFINITY ? 0.f : p1 * vf[nb].y;
+            }
+            const uint32_t hi = pack_bf16(p0, p1);
+            const float2 hf = bf2_to_f2(hi);
+            const uint32_t lo = pack_bf16(p0 - hf.x, p1 - hf.y);
+            if (GP == 4) {
+              ph[r][nb] = g < 4 ? hi : lo;     // rows 4..7 repeat the heads: they carry the low terms
+            } else {
+              ph[r][nb] = hi;
+              pl[r][nb] = lo;
+            }
+          }
+        }
+        // ---- accumulators += V^T P^T: rows are head elements, columns queries ----
+        if constexpr (!E4M3) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            uint32_t f[4];
+            ldsm_x4_t(at(vs, (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), f);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              mma_bf16_16816(acc[r][k], f, ph[r][0], ph[r][1]);
+              if (GP != 4) mma_bf16_16816(acc[r][k], f, pl[r][0], pl[r][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < KS; k += 2) {
+            uint32_t f[4];
+            ldsm_x4_t(at(vs, (lane & 7) + (((lane >> 3) & 1) << 3), k + (lane >> 4)), f);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t v[4];
+              e4m3_to_bf16(f[2 * c], v[0], v[1]);
+              e4m3_to_bf16(f[2 * c + 1], v[2], v[3]);
+#pragma unroll
+              for (int r = 0; r < R; ++r) {
+                mma_bf16_16816(acc[r][k + c], v, ph[r][0], ph[r][1]);
+                if (GP != 4) mma_bf16_16816(acc[r][k + c], v, pl[r][0], pl[r][1]);
+              }
+            }
+          }
+        }
+      }
+      if (cleared) fence_proxy_async_smem();   // those stores come before the next copy into the stage
+      __syncwarp();
+      if (!dead) {
+        ++seq_c;
+        issue();
+      }
+    }
+
+    // ---- join the warps ----
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      const int row = g + 8 * r;
+      if (t == 0 && row < GP) {
+        float* o = mml + (warp * GP + row) * 4;
+        o[0] = m[r]; o[1] = l[r]; o[2] = any ? 1.f : 0.f;
+      }
+      if (any) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = acc[r][k][i];
+            if (GP == 4) v += __shfl_xor_sync(0xffffffffu, v, 2);    // high and low terms
+            const int q = 2 * t + (i & 1) + 8 * r;
+            const int e = k * 16 + (E4M3 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
+            if (q < GP) macc[(warp * GP + q) * D + e] = v;
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const bool complete = w.j == w.jlo && w.jend == w.jhi;
+    const int64_t unit = static_cast<int64_t>(w.b) * Hkv + w.h;
+    const int slot = 2 * static_cast<int>(blockIdx.x) + (w.index == share * blockIdx.x ? 0 : 1);
+    const int64_t orow = static_cast<int64_t>(w.b) * a.Hq + static_cast<int64_t>(w.h) * G;
+    for (int i = threadIdx.x; i < G * (D / 4); i += NW * 32) {
+      const int q = i / (D / 4), e = (i % (D / 4)) * 4;
+      float M = -INFINITY, seen = 0.f;
+#pragma unroll
+      for (int x = 0; x < NW; ++x) {
+        M = fmaxf(M, mml[(x * GP + q) * 4]);
+        seen += mml[(x * GP + q) * 4 + 2];
+      }
+      const float mu = M == -INFINITY ? 0.f : M;
+      float L = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < NW; ++x) {
+        if (mml[(x * GP + q) * 4 + 2] == 0.f) continue;
+        const float c = ex2(mml[(x * GP + q) * 4] - mu);
+        const float4 v = *reinterpret_cast<const float4*>(&macc[(x * GP + q) * D + e]);
+        L = fmaf(c, mml[(x * GP + q) * 4 + 1], L);
+        o.x = fmaf(c, v.x, o.x); o.y = fmaf(c, v.y, o.y); o.z = fmaf(c, v.z, o.z); o.w = fmaf(c, v.w, o.w);
+      }
+      if (complete) {
+        uint2 y = make_uint2(0u, 0u);
+        if (seen > 0.f) y = make_uint2(pack_bf16(o.x / L, o.y / L), pack_bf16(o.z / L, o.w / L));
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (orow + q) * D + e) = y;
+        if (a.lse && e == 0) a.lse[orow + q] = seen > 0.f ? (mu + log2f(L)) * kLn2 : -INFINITY;
+      } else {
+        __stcg(reinterpret_cast<float4*>(sc.acc + (static_cast<int64_t>(slot) * G + q) * D + e), o);
+        if (e == 0) __stcg(reinterpret_cast<float4*>(sc.ml + (static_cast<int64_t>(slot) * G + q) * 4), make_float4(M, L, seen, 0.f));
+      }
+    }
+    if (!complete) {
+      // ranges that hold a part of this unit
+      const int64_t ubeg = w.index - (w.j - w.jlo), uend = ubeg + (w.jhi - w.jlo);
+      const int c0 = static_cast<int>(ubeg / share), c1 = static_cast<int>((uend - 1) / share);
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) last_flag = atomicAdd(&sc.ticket[unit], 1) == c1 - c0;
+      __syncthreads();
+      if (last_flag) {
+        __threadfence();
+        if (threadIdx.x == 0) sc.ticket[unit] = 0;
+        for (int i = threadIdx.x; i < G * (D / 4); i += NW * 32) {
+          const int q = i / (D / 4), e = (i % (D / 4)) * 4;
+          float M = -INFINITY, L = 0.f, seen = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int c = c0; c <= c1; ++c) {
+            const int64_t sl = static_cast<int64_t>(2 * c + (c == c0 && ubeg != share * c ? 1 : 0)) * G + q;
+            const float4 ml = __ldcg(reinterpret_cast<const float4*>(sc.ml + sl * 4));
+            if (ml.z == 0.f) continue;
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(sc.acc + sl * D + e));
+            const float M1 = fmaxf(M, ml.x), mu = M1 == -INFINITY ? 0.f : M1;
+            const float ca = ex2(M - mu), cb = ex2(ml.x - mu);
+            M = M1; seen += ml.z;
+            L = L * ca + ml.y * cb;
+            o.x = o.x * ca + v.x * cb; o.y = o.y * ca + v.y * cb;
+            o.z = o.z * ca + v.z * cb; o.w = o.w * ca + v.w * cb;
+          }
+          uint2 y = make_uint2(0u, 0u);
+          if (seen > 0.f) y = make_uint2(pack_bf16(o.x / L, o.y / L), pack_bf16(o.z / L, o.w / L));
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (orow + q) * D + e) = y;
+          if (a.lse && e == 0) a.lse[orow + q] = seen > 0.f ? ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2 : -INFINITY;
+        }
+      }
+    }
+    __syncthreads();     // the join's buffers are free again
+    more = w.next(a, unit_step);
+  }
+  // copies that a dead warp leaves in flight: wait for them (bounded) before its shared memory goes
+  if (dead)
+    for (; seq_c < seq_p; ++seq_c) mbar_wait(&bars[seq_c % NST], (seq_c / NST) & 1);
+}
+
+// fp32 rows: one block per (sequence, query head); each warp walks every fourth
+// key with a running maximum and sum, and the warps are joined at the end.
+template <int D>
+__global__ void __launch_bounds__(NW * 32) attend_f32_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int E = D / 32;
+  __shared__ float sm_acc[NW][D], sm_m[NW], sm_l[NW];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int hq = blockIdx.x, b = blockIdx.y, h = hq / a.G;
+  const Span sp = span_of(a, b);
+  if (sp.n != a.lens[b] && threadIdx.x == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
   const int64_t qrow = static_cast<int64_t>(b) * a.Hq + hq;
+  const float* pages = reinterpret_cast<const float*>(a.pg.pages);
   float q[E], acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    q[e] = Elem<T>::to_f32(static_cast<const T*>(a.q)[qrow * D + lane * E + e]);
+    q[e] = static_cast<const float*>(a.q)[qrow * D + lane * E + e];
     acc[e] = 0.f;
   }
   float m = -INFINITY, sum = 0.f;
   bool any = false;
-  for (int i = lo + warp; i < n; i += kWarps) {
+  for (int i = sp.lo + warp; i < sp.n; i += NW) {
     const int page = a.table[b * a.table_stride + (i >> a.pg.page_shift)];
     if (page < 0 || page >= a.pg.n_pages) {
       if (lane == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
@@ -47,66 +680,107 @@ __global__ void __launch_bounds__(kWarps * 32) attend_simple_kernel(const __grid
     const int64_t vrow = krow + (1 << a.pg.page_shift);
     float s = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      float kx;
-      if (E4M3) kx = static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3*>(a.pg.pages)[krow * D + lane * E + e]);
-      else kx = Elem<T>::to_f32(reinterpret_cast<const T*>(a.pg.pages)[krow * D + lane * E + e]);
-      s = fmaf(q[e], kx, s);
-    }
+    for (int e = 0; e < E; ++e) s = fmaf(q[e], pages[krow * D + lane * E + e], s);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= a.scale * (E4M3 ? a.pg.scales[krow] : 1.f);
+    s *= a.scale;
     if (a.softcap > 0.f) s = a.softcap * tanhf(s / a.softcap);
     const float m1 = fmaxf(m, s);
     const float mu = m1 == -INFINITY ? 0.f : m1;
     const float c = expf(m - mu), p = expf(s - mu);
-    const float pv = p * (E4M3 ? a.pg.scales[vrow] : 1.f);
     sum = sum * c + p;
     m = m1;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      float vx;
-      if (E4M3) vx = static_cast<float>(reinterpret_cast<const __nv_fp8_e4m3*>(a.pg.pages)[vrow * D + lane * E + e]);
-      else vx = Elem<T>::to_f32(reinterpret_cast<const T*>(a.pg.pages)[vrow * D + lane * E + e]);
-      acc[e] = fmaf(pv, vx, acc[e] * c);
-    }
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(p, pages[vrow * D + lane * E + e], acc[e] * c);
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) sm_acc[warp][lane * E + e] = acc[e];
   if (lane == 0) { sm_m[warp] = m; sm_l[warp] = sum; }
   any = __syncthreads_or(any);
   float M = -INFINITY;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w]);
+  for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_m[w]);
   const float Mu = M == -INFINITY ? 0.f : M;
   float L = 0.f;
-  for (int w = 0; w < kWarps; ++w) L += sm_l[w] * expf(sm_m[w] - Mu);
-  for (int e = threadIdx.x; e < D; e += kWarps * 32) {
+  for (int w = 0; w < NW; ++w) L += sm_l[w] * expf(sm_m[w] - Mu);
+  for (int e = threadIdx.x; e < D; e += NW * 32) {
     float o = 0.f;
-    for (int w = 0; w < kWarps; ++w) o += sm_acc[w][e] * expf(sm_m[w] - Mu);
-    static_cast<T*>(a.out)[qrow * D + e] = Elem<T>::from_f32(any ? o / L : 0.f);
+    for (int w = 0; w < NW; ++w) o += sm_acc[w][e] * expf(sm_m[w] - Mu);
+    static_cast<float*>(a.out)[qrow * D + e] = any ? o / L : 0.f;
   }
   if (threadIdx.x == 0 && a.lse) a.lse[qrow] = any ? Mu + logf(L) : -INFINITY;
 }
 
-template <typename T, int D, bool E4M3>
-int attend_t(const AttendArgs& a, cudaStream_t st) {
-  attend_simple_kernel<T, D, E4M3><<<dim3(a.Hq, a.batch), kWarps * 32, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+}
+
+// Calls f with the kernel of (d, 8 bits, heads per KV head) and its shared memory.
+template <typename F>
+int with_kernel(int d, bool e8, int G, F f) {
+#define KVPOP_ATTEND(DD, EE, PP) \
+  if (d == DD && e8 == EE && G <= PP) return f(attend_kernel<DD, EE, PP>, Geo<DD, EE, PP>::SMEM);
+  KVPOP_ATTEND(128, false, 4) KVPOP_ATTEND(128, false, 8) KVPOP_ATTEND(128, false, 16)
+  KVPOP_ATTEND(128, true, 4) KVPOP_ATTEND(128, true, 8) KVPOP_ATTEND(128, true, 16)
+  KVPOP_ATTEND(64, false, 4) KVPOP_ATTEND(64, false, 8) KVPOP_ATTEND(64, false, 16)
+  KVPOP_ATTEND(64, true, 4) KVPOP_ATTEND(64, true, 8) KVPOP_ATTEND(64, true, 16)
+#undef KVPOP_ATTEND
+  return -2;
 }
 
 }  // namespace
 
-int launch_attend(const AttendArgs& a, int dtype, int d, int num_sms, cudaStream_t st) {
-  (void)num_sms;
+size_t attend_scratch_bytes(int G, int d, int units) {
+  return static_cast<size_t>(kAttendRanges) * 2 * G * (d + 4) * 4 + ((static_cast<size_t>(units) * 4 + 255) & ~static_cast<size_t>(255));
+}
+
+int make_attend_map(CUtensorMap* map, void* pages, int dtype, int d, bool e8, int page_size, int64_t page_heads) {
+  if (dtype != KVPOP_DTYPE_BF16) return 0;     // fp32 rows are not read through a map
+  const auto encode = tensor_map_encoder();
+  if (encode == nullptr) return -1;
+  const int es = e8 ? 1 : 2, row = d * es, part = row < 128 ? row : 128;
+  const cuuint64_t dim[5] = {static_cast<cuuint64_t>(part / es), static_cast<cuuint64_t>(page_size),
+                             static_cast<cuuint64_t>(row / part), 2, static_cast<cuuint64_t>(page_heads)};
+  const cuuint64_t stride[4] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(part),
+                                static_cast<cuuint64_t>(row) * page_size, static_cast<cuuint64_t>(row) * page_size * 2};
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(part / es), 16, static_cast<cuuint32_t>(row / part), 2, 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  const CUresult r = encode(map, e8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, pages, dim,
+                            stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            part == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : -1;
+}
+
+int prepare_attend(int dtype, int d, bool e8, int G) {
+  if (dtype != KVPOP_DTYPE_BF16) return 0;
+  return with_kernel(d, e8, G, [](auto kernel, int smem) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess ? 0 : -1;
+  });
+}
+
+int launch_attend(const CUtensorMap& map, const AttendArgs& a, void* scratch, int dtype, int d, int num_sms,
+                  cudaStream_t st) {
   const bool e8 = a.pg.scales != nullptr;
-  if (dtype == KVPOP_DTYPE_BF16) {
-    if (d == 128) return e8 ? attend_t<__nv_bfloat16, 128, true>(a, st) : attend_t<__nv_bfloat16, 128, false>(a, st);
-    if (d == 64) return e8 ? attend_t<__nv_bfloat16, 64, true>(a, st) : attend_t<__nv_bfloat16, 64, false>(a, st);
-  } else if (!e8) {
-    if (d == 128) return attend_t<float, 128, false>(a, st);
-    if (d == 64) return attend_t<float, 64, false>(a, st);
+  if (dtype == KVPOP_DTYPE_F32) {
+    if (e8 || (d != 64 && d != 128)) return -2;
+    if (d == 128) attend_f32_kernel<128><<<dim3(a.Hq, a.batch), NW * 32, 0, st>>>(a);
+    else attend_f32_kernel<64><<<dim3(a.Hq, a.batch), NW * 32, 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
   }
-  return -2;
+  AttendScratch sc;
+  sc.acc = static_cast<float*>(scratch);
+  sc.ml = sc.acc + static_cast<size_t>(kAttendRanges) * 2 * a.G * d;
+  sc.ticket = reinterpret_cast<int32_t*>(sc.ml + static_cast<size_t>(kAttendRanges) * 2 * a.G * 4);
+  const int grid = kCtasPerSm * num_sms < kAttendRanges ? kCtasPerSm * num_sms : kAttendRanges;
+  return with_kernel(d, e8, a.G, [&](auto kernel, int smem) {
+    kernel<<<grid, NW * 32, smem, st>>>(map, a, sc);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  });
 }
 
 }  // namespace kvpop

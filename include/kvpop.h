@@ -447,7 +447,7 @@ typedef struct kvpop_paged_config {
   int32_t n_kv_heads;    /* 1..1024 */
   int32_t head_dim;      /* 64 or 128 */
   int32_t page_size;     /* tokens of a page: 16, 32, 64, 128 or 256 */
-  int32_t n_pages;       /* pages of each layer; n_pages * page_size < 2^31 */
+  int32_t n_pages;       /* pages of each layer; n_pages * page_size and n_pages * n_kv_heads < 2^31 */
   int32_t max_batch;     /* most sequences of one kvpop_paged_attend: 1..1024 */
   int32_t dtype;         /* of q, k, v and outputs: KVPOP_DTYPE_* */
   int32_t cache_format;  /* KVPOP_CACHE_* */
@@ -527,7 +527,8 @@ typedef struct kvpop_attend_options {
  * the cache's length and joined in a fixed order, so equal calls give equal
  * bits.  q, out: device [batch][n_q_heads][head_dim] in dtype, 16-byte
  * aligned; lse: device fp32 [batch][n_q_heads] receiving log sum_j e^(s_j),
- * or NULL.  page_table, lens as kvpop_paged_gather; 0 <= batch <= max_batch.
+ * or NULL.  page_table, lens as kvpop_paged_gather; 0 <= batch <= max_batch,
+ * table_width * page_size <= 2^30.
  * A sequence with no token gets out = 0, lse = -inf.  Infinities and NaN in
  * tokens that are not attended do not reach the result; a NaN or +inf score
  * gives NaN.  A length that is negative or past table_width * page_size

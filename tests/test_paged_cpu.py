@@ -182,3 +182,76 @@ def test_binding_refuses_host_tensors_and_bad_rope():
         kp._rows([1.0], "q", (1,), torch.float32, dev)
     with pytest.raises(ValueError, match="int32"):
         kp._ints(torch.zeros(3, dtype=torch.int64), "slots", (3,), dev)
+
+
+# ---- the attention's work split, restated from kvpop_paged_attn.cu ----
+
+NW, MIN_SHARE, UNIT_BLOCKS = 4, 8, 16
+
+
+def _walk(blocks, hkv, n_cta):
+    """Every CTA's segments: (cta, unit, j, jend, jlo..jhi = 0..blocks, index) and the share (None: whole units)."""
+    total, longest = sum(blocks) * hkv, max(blocks, default=0)
+    if longest <= UNIT_BLOCKS:
+        return [(u % n_cta, u, 0, blocks[u // hkv], 0) for u in range(len(blocks) * hkv) if blocks[u // hkv]], None
+    share = max(-(-total // n_cta), MIN_SHARE)
+    segs = []
+    for c in range(n_cta):
+        beg = share * c
+        if beg >= total:
+            break
+        before = b = 0
+        while before + blocks[b] * hkv <= beg:
+            before += blocks[b] * hkv
+            b += 1
+        h, j = divmod(beg - before, blocks[b])
+        left, index = min(share, total - beg), beg
+        while left > 0:
+            jend = min(blocks[b], j + left)
+            segs.append((c, b * hkv + h, j, jend, index))
+            left -= jend - j
+            index += jend - j
+            if left <= 0:
+                break
+            h += 1
+            if h == hkv:
+                h = 0
+                b += 1
+                while not blocks[b]:
+                    b += 1
+            j = 0
+    return segs, share
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_attention_work_split(seed):
+    """Every block of every unit is covered once; a warp's blocks of a segment
+    partition it; the ranges that the last arriver reads are those that wrote,
+    each from its own slot."""
+    rng = np.random.default_rng(seed)
+    hkv, n_cta = int(rng.choice([1, 2, 8])), int(rng.choice([4, 296, 512]))
+    blocks = [int(x) for x in rng.integers(0, rng.choice([5, 17, 40, 700]), size=rng.integers(1, 30))]
+    segs, share = _walk(blocks, hkv, n_cta)
+    cover = {u: [] for u in range(len(blocks) * hkv)}
+    slots, parts = set(), {}
+    for c, u, j, jend, index in segs:
+        assert jend > j
+        cover[u].append((j, jend))
+        own = [list(range(j + ((w - index) & (NW - 1)), jend, NW)) for w in range(NW)]
+        assert sorted(sum(own, [])) == list(range(j, jend))
+        if share is not None and (j, jend) != (0, blocks[u // hkv]):
+            ubeg = index - j
+            c0, c1 = ubeg // share, (ubeg + blocks[u // hkv] - 1) // share
+            slot = 2 * c + (0 if index == share * c else 1)
+            assert slot not in slots and c0 <= c <= c1 < n_cta
+            slots.add(slot)
+            assert slot == 2 * c + (1 if c == c0 and ubeg != share * c else 0)      # as the last arriver computes it
+            parts[u] = c1 - c0 + 1
+    for u, n in cover.items():
+        n.sort()
+        at = 0
+        for lo, hi in n:
+            assert lo == at
+            at = hi
+        assert at == blocks[u // hkv]
+        assert parts.get(u, 1) == max(len(n), 1)
