@@ -19,6 +19,8 @@ import os
 import struct
 from typing import Optional
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # KVPOP_LIBRARY may point at another build of the same library (e.g. a tuning variant).
 LIB_PATH = os.environ.get("KVPOP_LIBRARY") or os.path.join(_HERE, "libkvpop.so")
@@ -456,19 +458,20 @@ class KVPopCache:
 
 # ---- heads of new tokens, and the paged (full) cache ----
 
+# These calls are made once per layer and token, and the kernels behind the
+# small ones run for 3 to 6 us: the checks below read each attribute once.
+
 def _stream_on(device, stream) -> Optional[int]:
     """The given stream, or `device`'s current one (which need not be the current device's)."""
-    if stream is None:
-        import torch
-        stream = torch.cuda.current_stream(device)
-    return stream.cuda_stream or None
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _rows(t, name: str, shape, dtype, device, written: bool = False) -> bytes:
     """A kvpop_rows of `t`, rows [batch][token][head][head_dim] with the last
     dimension contiguous: any strides of whole 16 bytes.  Raises ValueError on
     anything else; the C ABI sees only addresses."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.device != device or device.type != "cuda":
@@ -478,20 +481,30 @@ def _rows(t, name: str, shape, dtype, device, written: bool = False) -> bytes:
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     sb, st, sh, sd = t.stride()
-    b, n, h, _ = shape
-    unit = 16 // t.element_size()
-    bad = sd != 1 or (b > 1 and sb % unit) or (n > 1 and st % unit) or (h > 1 and sh % unit) or t.data_ptr() % 16
-    if bad and b and n:
-        raise ValueError(f"{name}: strides {t.stride()} at {t.data_ptr():#x}: rows must be contiguous and start on "
-                         "16 bytes")
-    if written and b and n and ((b > 1 and not sb) or (n > 1 and not st) or (h > 1 and not sh)):
-        raise ValueError(f"{name}: an expanded tensor cannot be written")
-    return _pack_rows(t.data_ptr(), sb, st, sh)
+    at = t.data_ptr()
+    unit = 4 if dtype is torch.float32 else 8
+    if sd != 1 or at & 15 or (sb | st | sh) % unit or (written and not (sb and st and sh)):
+        # something is odd; strides of dimensions of one row or none do not count
+        b, n, h, _ = shape
+        used = [s for s, m in ((sb, b), (st, n), (sh, h)) if m > 1]
+        if b and n:
+            if sd != 1 or at & 15 or any(s % unit for s in used):
+                raise ValueError(f"{name}: strides {t.stride()} at {at:#x}: rows must be contiguous and start on "
+                                 "16 bytes")
+            if written and not all(used):
+                raise ValueError(f"{name}: an expanded tensor cannot be written")
+    return _pack_rows(at, sb, st, sh)
+
+
+def _dense(t, name: str, shape, dtype, device) -> None:
+    """check_tensor, with its message for anything that is not as it should be."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        check_tensor(t, name, shape, dtype, device)
 
 
 def _ints(t, name: str, shape, device) -> int:
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.shape != shape or t.device != device \
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.shape != shape or t.device != device \
             or not t.is_contiguous():
         what = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
         raise ValueError(f"{name}: expected a contiguous int32 tensor {tuple(shape)} on {device}, got {what}")
@@ -519,7 +532,6 @@ def make_rope(inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6, scal
     weights, or None for heads that are not normalised.  eps is added to the
     mean square; scale multiplies cosine and sine.  interleaved: pairs
     (2i, 2i + 1) instead of (i, i + rot_dim / 2)."""
-    import torch
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.device.type != "cuda":
         raise ValueError("inv_freq: expected a cuda tensor")
     if inv_freq.dim() != 1 or inv_freq.numel() % 4:
@@ -551,7 +563,6 @@ def qk_norm_rope(rope: Rope, q, k, positions, q_out, k_out, stream=None) -> None
     heads; any strides of whole 16 bytes (views of a projection's output,
     transposed views of head-major buffers), q_out = q and k_out = k among
     them.  positions: int32 [batch][tokens]."""
-    import torch
     if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.device.type != "cuda":
         raise ValueError("q: expected a cuda tensor [batch][tokens][heads][head_dim]")
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
@@ -559,7 +570,7 @@ def qk_norm_rope(rope: Rope, q, k, positions, q_out, k_out, stream=None) -> None
     dtype, device, qs = q.dtype, q.device, q.shape
     b, n, hq, d = qs
     hkv = k.shape[2]
-    ks = torch.Size((b, n, hkv, d))
+    ks = (b, n, hkv, d)
     _check_rope(rope, d, device)
     _check(lib.kvpop_qk_norm_rope(dtype_code(dtype), d, hq, hkv, rope.packed, b, n,
                                   _rows(q, "q", qs, dtype, device), _rows(k, "k", ks, dtype, device),
@@ -594,12 +605,12 @@ class KVPopPagedCache:
     events."""
 
     def __init__(self, cfg: kvpop_paged_config, device=None, library=None):
-        import torch
         self.cfg = cfg
         self._lib = library or lib
         self.nbytes = paged_bytes(cfg, self._lib)
         self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device or "cuda")
         self.device = self.buffer.device
+        self._kv = (cfg.n_kv_heads, cfg.head_dim)
         base = self.buffer.data_ptr()
         self._off = (-base) % 256
         self.handle = ctypes.c_void_p()
@@ -607,6 +618,12 @@ class KVPopPagedCache:
             _check(self._lib.kvpop_paged_create(ctypes.byref(cfg), ctypes.c_void_p(base + self._off), self.nbytes,
                                                 ctypes.byref(self.handle)), "kvpop_paged_create")
         self.dtype = _torch_dtype(cfg.dtype)
+        lay, e8 = self.layout(), cfg.cache_format == KVPOP_CACHE_E4M3
+        shape = (cfg.n_pages, cfg.n_kv_heads, 2, cfg.page_size, cfg.head_dim)
+        held = torch.float8_e4m3fn if e8 else self.dtype
+        self._pages = [self._view(lay.pages_offset + i * lay.pages_layer_stride, shape, held) for i in range(cfg.n_layers)]
+        self._scales = [self._view(lay.scales_offset + i * lay.scales_layer_stride, shape[:-1], torch.float32)
+                        if e8 else None for i in range(cfg.n_layers)]
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -615,10 +632,9 @@ class KVPopPagedCache:
             self.handle = None
 
     def _kv_shape(self, t, name):
-        import torch
         if not isinstance(t, torch.Tensor) or t.dim() != 4:
             raise ValueError(f"{name}: expected a cuda tensor [batch][tokens][heads][head_dim]")
-        return torch.Size((t.shape[0], t.shape[1], self.cfg.n_kv_heads, self.cfg.head_dim))
+        return t.shape[:2] + self._kv
 
     def append(self, layer: int, k, v, slots, stream=None) -> None:
         """Writes keys and values, [batch][tokens][KV heads][head_dim], to the
@@ -634,10 +650,9 @@ class KVPopPagedCache:
     def append_qkv(self, layer: int, rope: Rope, q, k, v, positions, slots, q_out, stream=None) -> None:
         """qk_norm_rope and append in one launch: normalised and turned queries
         go to q_out, keys and values to their slots."""
-        import torch
         shape = self._kv_shape(k, "k")
         b, n, d = shape[0], shape[1], shape[3]
-        qs = torch.Size((b, n, self.cfg.n_q_heads, d))
+        qs = (b, n, self.cfg.n_q_heads, d)
         _check_rope(rope, d, self.device)
         _check(self._lib.kvpop_paged_append_qkv(self.handle, layer, rope.packed,
                                                 _rows(q, "q", qs, self.dtype, self.device),
@@ -649,7 +664,6 @@ class KVPopPagedCache:
                                                 _stream_on(self.device, stream)), "kvpop_paged_append_qkv")
 
     def _table(self, page_table, lens, b):
-        import torch
         if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
             raise ValueError("page_table: expected an int32 cuda tensor [batch][pages]")
         width = page_table.shape[1]
@@ -674,16 +688,15 @@ class KVPopPagedCache:
         [head_dim]; lse fp32 [batch][q heads] or None.  scale 0: 1 / sqrt(head_dim);
         softcap > 0: scores become softcap * tanh(score / softcap); window > 0:
         the last `window` tokens alone are attended."""
-        import torch
         c = self.cfg
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q: expected a cuda tensor [batch][q heads][head_dim]")
         b = q.shape[0]
-        shape = torch.Size((b, c.n_q_heads, c.head_dim))
-        check_tensor(q, "q", shape, self.dtype, self.device)
-        check_tensor(out, "out", shape, self.dtype, self.device)
+        shape, device = (b, c.n_q_heads, c.head_dim), self.device
+        _dense(q, "q", shape, self.dtype, device)
+        _dense(out, "out", shape, self.dtype, device)
         if lse is not None:
-            check_tensor(lse, "lse", shape[:2], torch.float32, self.device)
+            _dense(lse, "lse", shape[:2], torch.float32, device)
         table, width, lens_p = self._table(page_table, lens, b)
         _check(self._lib.kvpop_paged_attend(self.handle, layer, q.data_ptr(), table, width, width, lens_p, b,
                                             _pack_attend_options(scale, softcap, window), out.data_ptr(), _ptr(lse),
@@ -696,27 +709,18 @@ class KVPopPagedCache:
         start = self._off + offset
         return self.buffer[start:start + n].view(dtype).view(shape)
 
-    def _layer_view(self, layer, offset, stride, shape, dtype):
-        if not 0 <= layer < self.cfg.n_layers:
-            raise ValueError(f"layer {layer}: the cache has {self.cfg.n_layers}")
-        return self._view(offset + layer * stride, shape, dtype)
+    def _layer(self, views, layer):
+        if not 0 <= layer < len(views):
+            raise ValueError(f"layer {layer}: the cache has {len(views)}")
+        return views[layer]
 
     def pages(self, layer: int):
         """Layer `layer`'s held rows, [pages][KV heads][2 (key, value)][page_size][head_dim]: a view."""
-        import torch
-        c, lay = self.cfg, self.layout()
-        dtype = torch.float8_e4m3fn if c.cache_format == KVPOP_CACHE_E4M3 else self.dtype
-        return self._layer_view(layer, lay.pages_offset, lay.pages_layer_stride,
-                                (c.n_pages, c.n_kv_heads, 2, c.page_size, c.head_dim), dtype)
+        return self._layer(self._pages, layer)
 
     def scales(self, layer: int):
         """The scales of layer `layer`'s rows, [pages][KV heads][2][page_size]: a view; None without them."""
-        import torch
-        c, lay = self.cfg, self.layout()
-        if c.cache_format != KVPOP_CACHE_E4M3:
-            return None
-        return self._layer_view(layer, lay.scales_offset, lay.scales_layer_stride,
-                                (c.n_pages, c.n_kv_heads, 2, c.page_size), torch.float32)
+        return self._layer(self._scales, layer)
 
     def layout(self) -> kvpop_paged_layout_info:
         info = kvpop_paged_layout_info()
