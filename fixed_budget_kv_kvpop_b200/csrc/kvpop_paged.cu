@@ -24,6 +24,17 @@ template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bflo
   const float2 lo = bf2_to_f2(r.x), hi = bf2_to_f2(r.y);
   x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
 }
+// The same held as they are loaded, for rows that wait their turn.
+template <typename T> struct Raw4;
+template <> struct Raw4<float> { float4 v; };
+template <> struct Raw4<__nv_bfloat16> { uint2 v; };
+__device__ __forceinline__ void unpack4(const Raw4<float>& r, float* x) {
+  x[0] = r.v.x; x[1] = r.v.y; x[2] = r.v.z; x[3] = r.v.w;
+}
+__device__ __forceinline__ void unpack4(const Raw4<__nv_bfloat16>& r, float* x) {
+  const float2 lo = bf2_to_f2(r.v.x), hi = bf2_to_f2(r.v.y);
+  x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
+}
 template <typename T> __device__ __forceinline__ void store4(T* p, const float* x);
 template <> __device__ __forceinline__ void store4<float>(float* p, const float* x) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
@@ -55,131 +66,255 @@ __device__ __forceinline__ void turn_of(int pos, double inv_freq, float scale, f
   s *= scale;
 }
 
+// e4m3(x / scale) of eight elements.  The quotients have to be the rounded
+// ones: bf16 rows often put them on the middle between two held values, and a
+// product with the reciprocal would send those to either side.  With r the
+// rounded reciprocal, q = x r is off by an ulp or so, and q + (x - q scale) r,
+// the remainder being exact in one FMA, is the rounded quotient (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990); compared with the division for every bf16 significand and 2^23 scales.
+// Below 2^-90 the remainder could underflow: those rows divide.
+__device__ __forceinline__ void quotients(float (&x)[8], float scale) {
+  if (scale == 0.f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+  } else if (scale < 8.0779357e-28f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = x[e] / scale;
+  } else {
+    const float r = 1.f / scale;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float q = x[e] * r;
+      x[e] = fmaf(fmaf(-q, scale, x[e]), r, q);
+    }
+  }
+}
+
+// Scale of a row whose largest magnitude is m.
+__device__ __forceinline__ float scale_of(float m) {
+  const float scale = m * kPerStep;
+  if (!(scale < __int_as_float(0x7f800000))) return __int_as_float(0x7fffffff);   // inf or NaN: the row reads back as NaN
+  return scale < 1.17549435e-38f ? 0.f : scale;                                   // subnormal: held as zeros
+}
+
+// Row `slot` of a page range: index of head h's key (kv = 0) or value row.
+__device__ __forceinline__ int64_t page_row(const PagedLayer& pg, int64_t slot, int h, int kv) {
+  return ((((slot >> pg.page_shift) * pg.Hkv + h) * 2 + kv) << pg.page_shift) + (slot & ((1 << pg.page_shift) - 1));
+}
+
+// Heads of new tokens: norm, rotation, and with HEADS_STEP the write into pages.
+// Bound by HBM (every row is read and written once).  wpt warps share a token:
+// its cosines and sines (fp64 angles) are formed once, by different lanes, and
+// handed over in shared memory, while the rows' loads, up to U per lane, are
+// already on their way.
 template <typename T, int D, bool E4M3, int MODE>
-__global__ void __launch_bounds__(kThreads) heads_kernel(const __grid_constant__ HeadsArgs a, int passes, int chunk) {
+__global__ void __launch_bounds__(kThreads, 3) heads_kernel(const __grid_constant__ HeadsArgs a, int passes, int wpt_shift) {
   constexpr int LPR = D / 8;          // lanes per row
   constexpr int RPW = 32 / LPR;       // rows per warp and pass
-  const int lane = threadIdx.x & 31;
+  constexpr int U = 4;
+  __shared__ __align__(16) float2 turns[2][kThreads / 32][D / 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % LPR, sub = lane / LPR;
-  const int64_t n_items = static_cast<int64_t>(a.batch) * a.n_tokens * ((passes + chunk - 1) / chunk);
-  const int nch = (passes + chunk - 1) / chunk;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32; item < n_items;
-       item += static_cast<int64_t>(gridDim.x) * (kThreads / 32)) {
-    const int64_t t = item / nch;
-    const int p0 = static_cast<int>(item % nch) * chunk;
-    const int p1 = min(passes, p0 + chunk);
-    const int b = static_cast<int>(t / a.n_tokens), i = static_cast<int>(t % a.n_tokens);
+  const int wpt = 1 << wpt_shift;
+  const int seat = warp >> wpt_shift, wt = warp & (wpt - 1), seats = (kThreads / 32) >> wpt_shift;
+  const int tokens = a.batch * a.n_tokens;
+  const int rot = a.rope.rot;
+  const bool inter = a.rope.interleaved != 0;
+  const int n_rows = a.Hq + a.Hkv * (MODE == HEADS_DENSE ? 1 : 2);
+  // this lane's two element groups of a row, and their turns' places
+  int oa = 4 * l, ob = D / 2 + 4 * l;
+  if (!inter && rot < D) {
+    const int j = l - rot / 8;
+    oa = j < 0 ? 4 * l : rot + 4 * j;
+    ob = j < 0 ? 4 * l + rot / 2 : rot + (D - rot) / 2 + 4 * j;
+  }
+  const int pa = inter ? oa / 2 : oa, pb = inter ? ob / 2 : oa + 2;   // pairs pa, pa + 1 and pb, pb + 1
 
+  int buf = 0;
+  for (int t0 = blockIdx.x * seats; t0 < tokens; t0 += gridDim.x * seats, buf ^= 1) {
+    const int t = t0 + seat;
+    const bool live = t < tokens;
+    const int b = live ? t / a.n_tokens : 0, i = live ? t - b * a.n_tokens : 0;
+    const T* qrow = reinterpret_cast<const T*>(a.q.p) + b * a.q.bs + i * a.q.ts;
+    const T* krow = reinterpret_cast<const T*>(a.k.p) + b * a.k.bs + i * a.k.ts;
+    const T* vrow = MODE == HEADS_DENSE ? nullptr : reinterpret_cast<const T*>(a.v.p) + b * a.v.bs + i * a.v.ts;
+    bool turned = false;
+    float4 ca, cb;
     int64_t slot = -1;
-    if (MODE != HEADS_DENSE) {
-      const int s = a.slots[t];
-      if (s >= 0) {
-        if ((s >> a.pg.page_shift) < a.pg.n_pages) slot = s;
-        else if (lane == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
+    for (int p0 = wt; p0 < passes || (p0 == wt); p0 += U * wpt) {
+      Raw4<T> xa[U], xb[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = (p0 + u * wpt) * RPW + sub;
+        if (live && r < n_rows) {
+          const T* src = r < a.Hq ? qrow + r * a.q.hs
+                                  : r < a.Hq + a.Hkv ? krow + (r - a.Hq) * a.k.hs : vrow + (r - a.Hq - a.Hkv) * a.v.hs;
+          xa[u] = *reinterpret_cast<const Raw4<T>*>(src + oa);
+          xb[u] = *reinterpret_cast<const Raw4<T>*>(src + ob);
+        }
       }
-    }
-    // this lane's two element groups of a turned row, and their four turns
-    int oa = 4 * l, ob = D / 2 + 4 * l;
-    float cs[4], sn[4];
-    if (MODE != HEADS_APPEND) {
-      const int rot = a.rope.rot;
-      const int pos = a.pos[t];
-      const bool inter = a.rope.interleaved != 0;
-      if (!inter && rot < D) {
-        const int j = l - rot / 8;
-        oa = j < 0 ? 4 * l : rot + 4 * j;
-        ob = j < 0 ? 4 * l + rot / 2 : rot + (D - rot) / 2 + 4 * j;
+      if (!turned) {
+        turned = true;
+        if (live) {
+          const int pos = a.pos[t];
+          for (int p = wt * 32 + lane; p < rot / 2; p += wpt * 32) {
+            float2 cs;
+            turn_of(pos, a.rope.inv_freq[p], a.rope.scale, cs.x, cs.y);
+            turns[buf][seat][p] = cs;
+          }
+          if (MODE == HEADS_STEP) {
+            const int s = a.slots[t];
+            if (s >= 0) {
+              if ((s >> a.pg.page_shift) < a.pg.n_pages) slot = s;
+              else if (lane == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
+            }
+          }
+        }
+        __syncthreads();
+        ca = pa < rot / 2 ? *reinterpret_cast<const float4*>(&turns[buf][seat][pa]) : make_float4(1.f, 0.f, 1.f, 0.f);
+        cb = pb < rot / 2 ? *reinterpret_cast<const float4*>(&turns[buf][seat][pb]) : make_float4(1.f, 0.f, 1.f, 0.f);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // pair index: (p, p + rot / 2), or (2p, 2p + 1)
-        const int p = inter ? ((e < 2 ? oa : ob) / 2 + (e & 1)) : oa + e;
-        const bool turned = inter ? p < rot / 2 : oa < rot / 2;
-        cs[e] = 1.f; sn[e] = 0.f;
-        if (turned) turn_of(pos, a.rope.inv_freq[p], a.rope.scale, cs[e], sn[e]);
-      }
-    }
-    const int n_rows = (MODE == HEADS_APPEND ? 0 : a.Hq) + a.Hkv * (MODE == HEADS_DENSE ? 1 : 2);
-    for (int p = p0; p < p1; ++p) {
-      const int r = p * RPW + sub;
-      const bool live = r < n_rows;
-      // row kinds: queries, keys, values
-      const int rq = MODE == HEADS_APPEND ? 0 : a.Hq;
-      const int kind = r < rq ? 0 : r < rq + a.Hkv ? 1 : 2;
-      const int h = kind == 0 ? r : kind == 1 ? r - rq : r - rq - a.Hkv;
-      const RowsView& src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-      const bool todo = live && (kind == 0 || MODE == HEADS_DENSE || slot >= 0);
-      const bool turn = MODE != HEADS_APPEND && kind < 2;
-      const int ea = turn ? oa : 4 * l, eb = turn ? ob : D / 2 + 4 * l;
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.f;
-      if (todo) {
-        const T* row = reinterpret_cast<const T*>(src.p) + b * src.bs + i * src.ts + h * src.hs;
-        load4<T>(row + ea, x);
-        load4<T>(row + eb, x + 4);
-      }
-      if (MODE != HEADS_APPEND) {
+      for (int u = 0; u < U; ++u) {
+        const int r = (p0 + u * wpt) * RPW + sub;
+        if ((p0 + u * wpt) * RPW >= n_rows) break;
+        const int kind = r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;    // query, key, value
+        const int h = kind == 0 ? r : kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
+        const bool on = live && r < n_rows;
+        float y[8];
         float ss = 0.f;
+        if (on) {
+          unpack4(xa[u], y);
+          unpack4(xb[u], y + 4);
+        }
+        if (on && kind < 2) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+          for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
+        }
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float* w = kind == 0 ? a.rope.q_weight : a.rope.k_weight;
-        if (turn && w != nullptr && todo) {
-          const float rn = rsqrtf(ss * (1.f / D) + a.rope.eps);
-          float wv[8];
-          load4<float>(w + ea, wv);
-          load4<float>(w + eb, wv + 4);
+        if (kind < 2 && on) {
+          const float* w = kind == 0 ? a.rope.q_weight : a.rope.k_weight;
+          if (w != nullptr) {
+            const float rn = rsqrtf(ss * (1.f / D) + a.rope.eps);
+            float wv[8];
+            load4<float>(w + oa, wv);
+            load4<float>(w + ob, wv + 4);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = x[e] * rn * wv[e];
-        }
-        if (turn) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float& u = a.rope.interleaved ? x[2 * e] : x[e];
-            float& v = a.rope.interleaved ? x[2 * e + 1] : x[e + 4];
-            const float u0 = u, v0 = v;
-            u = u0 * cs[e] - v0 * sn[e];
-            v = v0 * cs[e] + u0 * sn[e];
+            for (int e = 0; e < 8; ++e) y[e] = y[e] * rn * wv[e];
+          }
+          auto turn = [](float& p, float& q, float c, float s) {
+            const float p0 = p, q0 = q;
+            p = p0 * c - q0 * s;
+            q = q0 * c + p0 * s;
+          };
+          if (inter) {
+            turn(y[0], y[1], ca.x, ca.y); turn(y[2], y[3], ca.z, ca.w);
+            turn(y[4], y[5], cb.x, cb.y); turn(y[6], y[7], cb.z, cb.w);
+          } else {
+            turn(y[0], y[4], ca.x, ca.y); turn(y[1], y[5], ca.z, ca.w);
+            turn(y[2], y[6], cb.x, cb.y); turn(y[3], y[7], cb.z, cb.w);
           }
         }
-      }
-      if (kind == 0 || MODE == HEADS_DENSE) {
-        const RowsView& dst = kind == 0 ? a.qo : a.ko;
-        if (todo) {
+        if (on && (kind == 0 || MODE == HEADS_DENSE)) {
+          const RowsView& dst = kind == 0 ? a.qo : a.ko;
           T* row = reinterpret_cast<T*>(dst.p) + b * dst.bs + i * dst.ts + h * dst.hs;
-          store4<T>(row + ea, x);
-          store4<T>(row + eb, x + 4);
+          store4<T>(row + oa, y);
+          store4<T>(row + ob, y + 4);
+        }
+        if (MODE == HEADS_STEP) {
+          const bool keep = on && kind > 0 && slot >= 0;
+          const int64_t at = keep ? page_row(a.pg, slot, h, kind - 1) : 0;
+          if (E4M3) {
+            float m = 0.f;
+            if (keep) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(y[e]));
+            }
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (keep) {
+              const float scale = scale_of(m);
+              quotients(y, scale);
+              *reinterpret_cast<uint32_t*>(a.pg.pages + at * D + oa) = to_e4m3x4(y);
+              *reinterpret_cast<uint32_t*>(a.pg.pages + at * D + ob) = to_e4m3x4(y + 4);
+              if (l == 0) a.pg.scales[at] = scale;
+            }
+          } else if (keep) {
+            T* row = reinterpret_cast<T*>(a.pg.pages) + at * D;
+            store4<T>(row + oa, y);
+            store4<T>(row + ob, y + 4);
+          }
         }
       }
-      if (MODE != HEADS_DENSE) {
-        const int64_t page = slot >> a.pg.page_shift;
-        const int64_t prow = ((page * a.pg.Hkv + h) * 2 + (kind - 1)) << a.pg.page_shift;
-        const int64_t at = prow + (slot & ((1 << a.pg.page_shift) - 1));
-        if (E4M3) {
-          float m = 0.f;
+    }
+  }
+}
+
+// Eight consecutive elements as they lie in memory.
+template <typename T> struct Raw8;
+template <> struct Raw8<float> { float4 a, b; };
+template <> struct Raw8<__nv_bfloat16> { uint4 a; };
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float* x) { unpack16(r.a, x, __nv_bfloat16()); }
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float* x) {
+  x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
+  x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
+}
+
+// Keys and values of new tokens into pages.  Bound by HBM.  A warp takes `chunk`
+// passes of one token, RPW rows each, with U rows per lane on their way at a time.
+template <typename T, int D, bool E4M3>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ HeadsArgs a, int passes, int chunk) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
+  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+  const int nch = (passes + chunk - 1) / chunk;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+  const int64_t t = item / nch;
+  if (t >= static_cast<int64_t>(a.batch) * a.n_tokens) return;
+  const int p_beg = static_cast<int>(item - t * nch) * chunk, p_end = min(passes, p_beg + chunk);
+  const int b = static_cast<int>(t / a.n_tokens), i = static_cast<int>(t - static_cast<int64_t>(b) * a.n_tokens);
+  const T* krow = reinterpret_cast<const T*>(a.k.p) + b * a.k.bs + i * a.k.ts + 8 * l;
+  const T* vrow = reinterpret_cast<const T*>(a.v.p) + b * a.v.bs + i * a.v.ts + 8 * l;
+  const int s = a.slots[t];
+  for (int p0 = p_beg; p0 < p_end; p0 += U) {
+    Raw8<T> x[U];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(x[e]));
+    for (int u = 0; u < U; ++u) {
+      const int r = (p0 + u) * RPW + sub;
+      if (p0 + u < p_end && r < 2 * a.Hkv)
+        x[u] = *reinterpret_cast<const Raw8<T>*>(r < a.Hkv ? krow + r * a.k.hs : vrow + (r - a.Hkv) * a.v.hs);
+    }
+    if (s < 0) return;
+    if ((s >> a.pg.page_shift) >= a.pg.n_pages) {
+      if (lane == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
+      return;
+    }
 #pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-          if (todo && kind > 0) {
-            float scale = m * kPerStep;
-            if (!(scale < __int_as_float(0x7f800000))) scale = __int_as_float(0x7fffffff);   // inf or NaN: the row reads back as NaN
-            else if (scale < 1.17549435e-38f) scale = 0.f;                                   // held as zeros
-            // a true division: quotients that fall on the middle between two held values are common (both
-            // sides have few bits), and a product with the reciprocal would round those to either side
+    for (int u = 0; u < U; ++u) {
+      if (p0 + u >= p_end) break;
+      const int r = (p0 + u) * RPW + sub;
+      const bool on = r < 2 * a.Hkv;
+      const int kv = r < a.Hkv ? 0 : 1;
+      const int64_t at = on ? page_row(a.pg, s, r - kv * a.Hkv, kv) : 0;
+      if constexpr (E4M3) {
+        float y[8];
+        float m = 0.f;
+        if (on) {
+          unpack8(x[u], y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = scale == 0.f ? 0.f : x[e] / scale;
-            *reinterpret_cast<uint32_t*>(a.pg.pages + at * D + ea) = to_e4m3x4(x);
-            *reinterpret_cast<uint32_t*>(a.pg.pages + at * D + eb) = to_e4m3x4(x + 4);
-            if (l == 0) a.pg.scales[at] = scale;
-          }
-        } else if (todo && kind > 0) {
-          T* row = reinterpret_cast<T*>(a.pg.pages) + at * D;
-          store4<T>(row + ea, x);
-          store4<T>(row + eb, x + 4);
+          for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(y[e]));
         }
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (on) {
+          const float scale = scale_of(m);
+          quotients(y, scale);
+          *reinterpret_cast<uint2*>(a.pg.pages + at * D + 8 * l) = make_uint2(to_e4m3x4(y), to_e4m3x4(y + 4));
+          if (l == 0) a.pg.scales[at] = scale;
+        }
+      } else if (on) {
+        *reinterpret_cast<Raw8<T>*>(reinterpret_cast<T*>(a.pg.pages) + at * D + 8 * l) = x[u];
       }
     }
   }
@@ -244,16 +379,21 @@ int heads_t(const HeadsArgs& a, int mode, int num_sms, cudaStream_t st) {
   const int rpw = 32 / (D / 8);
   const int passes = (rows + rpw - 1) / rpw;
   const int64_t tokens = static_cast<int64_t>(a.batch) * a.n_tokens;
-  const int chunk = tokens >= 4 * num_sms ? passes : 1;
-  const int64_t warps = tokens * ((passes + chunk - 1) / chunk);
-  int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  if (grid > 1 << 20) grid = 1 << 20;
+  if (mode == HEADS_APPEND) {
+    const int chunk = tokens >= 4 * num_sms ? passes : 1;
+    const int64_t warps = tokens * ((passes + chunk - 1) / chunk);
+    const int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
+    append_kernel<T, D, E4M3><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, passes, chunk);
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  }
+  int shift = 0;      // warps per token: about three passes each
+  while (shift < 3 && (passes >> shift) > 3) ++shift;
+  const int seats = (kThreads / 32) >> shift;
+  const int64_t grid = (tokens + seats - 1) / seats;
   if (mode == HEADS_DENSE)
-    heads_kernel<T, D, false, HEADS_DENSE><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, passes, chunk);
-  else if (mode == HEADS_APPEND)
-    heads_kernel<T, D, E4M3, HEADS_APPEND><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, passes, chunk);
+    heads_kernel<T, D, false, HEADS_DENSE><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, passes, shift);
   else
-    heads_kernel<T, D, E4M3, HEADS_STEP><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, passes, chunk);
+    heads_kernel<T, D, E4M3, HEADS_STEP><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, passes, shift);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 

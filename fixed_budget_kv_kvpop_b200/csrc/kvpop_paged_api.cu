@@ -168,6 +168,7 @@ int kvpop_qk_norm_rope(int32_t dtype, int32_t head_dim, int32_t n_q_heads, int32
   int status;
   if (!rope_args(rope, head_dim, &a.rope, &status)) return status;
   if (batch == 0 || n_tokens == 0) return KVPOP_OK;
+  if (static_cast<int64_t>(batch) * n_tokens > (1 << 30)) return KVPOP_ERR_BAD_SHAPE;
   const int es = element_size(dtype);
   if (!positions || !aligned(positions, 4)) return KVPOP_ERR_INVALID_ARG;
   if (!rows_view(q, batch, n_tokens, n_q_heads, es, false, &a.q) ||
@@ -233,6 +234,7 @@ int kvpop_paged_append(kvpop_paged_handle* h, int32_t layer, const kvpop_rows* k
                        const int32_t* slots, int32_t batch, int32_t n_tokens, void* stream) {
   if (bad_layer(h, layer) || batch < 0 || n_tokens < 0) return KVPOP_ERR_INVALID_ARG;
   if (batch == 0 || n_tokens == 0) return KVPOP_OK;
+  if (static_cast<int64_t>(batch) * n_tokens > (1 << 30)) return KVPOP_ERR_BAD_SHAPE;
   const kvpop_paged_config& c = h->cfg;
   const int es = element_size(c.dtype);
   HeadsArgs a{};
@@ -259,6 +261,7 @@ int kvpop_paged_append_qkv(kvpop_paged_handle* h, int32_t layer, const kvpop_rop
   int status;
   if (!rope_args(rope, c.head_dim, &a.rope, &status)) return status;
   if (batch == 0 || n_tokens == 0) return KVPOP_OK;
+  if (static_cast<int64_t>(batch) * n_tokens > (1 << 30)) return KVPOP_ERR_BAD_SHAPE;
   if (!slots || !aligned(slots, 4) || !positions || !aligned(positions, 4)) return KVPOP_ERR_INVALID_ARG;
   if (!rows_view(q, batch, n_tokens, c.n_q_heads, es, false, &a.q) ||
       !rows_view(k, batch, n_tokens, c.n_kv_heads, es, false, &a.k) ||

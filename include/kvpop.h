@@ -428,7 +428,8 @@ typedef struct kvpop_rope {
 /* Norm and rotation of the heads of batch * n_tokens tokens.  q, q_out: rows
  * with n_q_heads heads; k, k_out: rows with n_kv_heads heads; positions:
  * device int32 [batch][n_tokens].  dtype KVPOP_DTYPE_*, head_dim 64 or 128.
- * Runs on the device that q lies on.  batch or n_tokens = 0 is a no-op.
+ * Runs on the device that q lies on.  batch or n_tokens = 0 is a no-op;
+ * batch * n_tokens <= 2^30.
  * Errors (nothing enqueued): KVPOP_ERR_INVALID_ARG (null or misaligned
  * pointer, bad stride, q not device memory, eps negative or not finite),
  * KVPOP_ERR_BAD_SHAPE; KVPOP_ERR_CUDA if the launch fails. */
@@ -484,7 +485,7 @@ int kvpop_paged_create(const kvpop_paged_config* cfg, void* dev_mem, size_t byte
  * zeros with scale 0; a row with an infinity or a NaN gets a NaN scale and
  * reads back as NaN.  Two tokens of one call must not share a slot (which
  * one's bytes stay would be undefined, element by element; other rows are
- * not touched).  n_tokens = 0 is a no-op.  Errors (nothing enqueued):
+ * not touched).  n_tokens = 0 is a no-op; batch * n_tokens <= 2^30.  Errors (nothing enqueued):
  * KVPOP_ERR_INVALID_ARG, KVPOP_ERR_BAD_SHAPE; KVPOP_ERR_CUDA. */
 int kvpop_paged_append(kvpop_paged_handle* h, int32_t layer, const kvpop_rows* k, const kvpop_rows* v,
                        const int32_t* slots, int32_t batch, int32_t n_tokens, void* stream);
