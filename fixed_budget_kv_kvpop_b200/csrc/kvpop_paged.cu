@@ -43,25 +43,26 @@ template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16*
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
 }
 
-// Maximum that keeps a NaN.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t to_e4m3x4(const float* x) {
   const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
   const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-// Cosine and sine of pos * inv_freq.  The angle is formed in fp64 as turns and
-// reduced to half a turn either way there, so far positions lose nothing:
-// at position 2^20 the fraction is off by about 2^20 * 2^-53 turns.
-__device__ __forceinline__ void turn_of(int pos, double inv_freq, float scale, float& c, float& s) {
-  const double t = static_cast<double>(pos) * (inv_freq * 0.15915494309189533577);
-  sincospif(2.f * static_cast<float>(t - rint(t)), &s, &c);
+// A frequency as the fraction of a turn per position, in units of 2^-64.
+// Products with a position wrap at whole turns, so the angle of any int32
+// position keeps all its bits (off by at most 2^-25 turns at 2^31, from the
+// frequency's own 53 bits), and no fp64 instruction is left per token: their
+// conversions ran at a sixteenth of the fp32 ones' rate and took 95% of the
+// conversion pipe's time.
+__device__ __forceinline__ uint64_t turn_step(double inv_freq) {
+  const double t = inv_freq * 0.15915494309189533577;
+  return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
+}
+__device__ __forceinline__ void turn_of(int pos, uint64_t step, float scale, float& c, float& s) {
+  const uint64_t at = static_cast<uint64_t>(static_cast<int64_t>(pos)) * step;
+  const float half_turns = static_cast<float>(static_cast<int32_t>(at >> 32)) * (1.f / 2147483648.f);
+  sincospif(half_turns, &s, &c);
   c *= scale;
   s *= scale;
 }
@@ -83,10 +84,13 @@ __device__ __forceinline__ void quotients(float (&x)[8], float scale) {
     for (int e = 0; e < 8; ++e) x[e] = x[e] / scale;
   } else {
     const float r = 1.f / scale;
+    const float2 r2 = make_float2(r, r), s2 = make_float2(-scale, -scale);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float q = x[e] * r;
-      x[e] = fmaf(fmaf(-q, scale, x[e]), r, q);
+    for (int e = 0; e < 8; e += 2) {
+      const float2 v = make_float2(x[e], x[e + 1]);
+      const float2 q = __fmul2_rn(v, r2);
+      const float2 y = ffma2(ffma2(q, s2, v), r2, q);
+      x[e] = y.x; x[e + 1] = y.y;
     }
   }
 }
@@ -98,150 +102,220 @@ __device__ __forceinline__ float scale_of(float m) {
   return scale < 1.17549435e-38f ? 0.f : scale;                                   // subnormal: held as zeros
 }
 
-// Row `slot` of a page range: index of head h's key (kv = 0) or value row.
-__device__ __forceinline__ int64_t page_row(const PagedLayer& pg, int64_t slot, int h, int kv) {
-  return ((((slot >> pg.page_shift) * pg.Hkv + h) * 2 + kv) << pg.page_shift) + (slot & ((1 << pg.page_shift) - 1));
+// Largest magnitude of eight elements as its bits: unsigned order is the order
+// of magnitudes, with infinities and then NaN on top.
+__device__ __forceinline__ uint32_t top_bits(const float (&x)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+  return m;
 }
 
-// Heads of new tokens: norm, rotation, and with HEADS_STEP the write into pages.
-// Bound by HBM (every row is read and written once).  wpt warps share a token:
-// its cosines and sines (fp64 angles) are formed once, by different lanes, and
-// handed over in shared memory, while the rows' loads, up to U per lane, are
-// already on their way.
-template <typename T, int D, bool E4M3, int MODE>
-__global__ void __launch_bounds__(kThreads, 3) heads_kernel(const __grid_constant__ HeadsArgs a, int passes, int wpt_shift) {
+// New tokens' heads.  HEADS_DENSE: queries and keys are normalised, turned and
+// written; HEADS_STEP: the same, but keys, and the values as they are, go into pages.
+//
+// Bound by HBM: every row is read and written once.  What stood in the way was
+// the number of instructions (265 a pass of two rows, 2.3 issued per cycle),
+// so all that does not depend on the token is done once: a warp keeps the same
+// heads for every token of its CTA (addresses, kinds), and the norm's weights
+// are multiplied into the token's cosines and sines, once per token, in shared
+// memory:  y = (x * wc + x_partner * ws) / rms.  The next token's rows are
+// loaded before the present one's are worked on.
+template <typename T, int D, bool E4M3, int MODE, bool INTER>
+__global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constant__ HeadsArgs a, int q_passes, int kv_passes, int wpt_shift) {
   constexpr int LPR = D / 8;          // lanes per row
   constexpr int RPW = 32 / LPR;       // rows per warp and pass
-  constexpr int U = 4;
-  __shared__ __align__(16) float2 turns[2][kThreads / 32][D / 2];
+  constexpr int U = 4;                // rows of a lane on their way
+  // [buffer][token of the CTA][query, key][wc, ws][element]
+  __shared__ __align__(16) float table[2][kThreads / 32][2][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % LPR, sub = lane / LPR;
-  const int wpt = 1 << wpt_shift;
+  const int wpt = 1 << wpt_shift;     // warps per token
   const int seat = warp >> wpt_shift, wt = warp & (wpt - 1), seats = (kThreads / 32) >> wpt_shift;
   const int tokens = a.batch * a.n_tokens;
   const int rot = a.rope.rot;
-  const bool inter = a.rope.interleaved != 0;
-  const int n_rows = a.Hq + a.Hkv * (MODE == HEADS_DENSE ? 1 : 2);
-  // this lane's two element groups of a row, and their turns' places
+  const int passes = q_passes + kv_passes * (MODE == HEADS_DENSE ? 1 : 2);
+  const int groups = (passes + U * wpt - 1) / (U * wpt);
+  // the lane's element groups [oa, oa + 4), [ob, ob + 4): partners are equal places of the two, or neighbours
   int oa = 4 * l, ob = D / 2 + 4 * l;
-  if (!inter && rot < D) {
+  if (!INTER && rot < D) {
     const int j = l - rot / 8;
     oa = j < 0 ? 4 * l : rot + 4 * j;
     ob = j < 0 ? 4 * l + rot / 2 : rot + (D - rot) / 2 + 4 * j;
   }
-  const int pa = inter ? oa / 2 : oa, pb = inter ? ob / 2 : oa + 2;   // pairs pa, pa + 1 and pb, pb + 1
+  const bool q_norm = a.rope.q_weight != nullptr, k_norm = a.rope.k_weight != nullptr;
 
+  // rows of a group: kind 0 query, 1 key, 2 value, 3 none
+  int kind[U], page_off[U];
+  bool on[U];
+  int64_t src_off[U], dst_off[U];
+  auto setup = [&](int grp) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int p = (grp * U + u) * wpt + wt;
+      kind[u] = p >= passes ? 3 : p < q_passes ? 0 : p < q_passes + kv_passes ? 1 : 2;
+      const int h = (kind[u] == 0 ? p : kind[u] == 1 ? p - q_passes : p - q_passes - kv_passes) * RPW + sub;
+      on[u] = kind[u] < 3 && h < (kind[u] == 0 ? a.Hq : a.Hkv);
+      src_off[u] = h * (kind[u] == 0 ? a.q.hs : kind[u] == 1 ? a.k.hs : a.v.hs);
+      dst_off[u] = h * (kind[u] == 0 ? a.qo.hs : a.ko.hs);
+      page_off[u] = (h * 2 + kind[u] - 1) << a.pg.page_shift;
+    }
+  };
+  Raw4<T> xa[U], xb[U];
+  auto load = [&](int t) {
+    const int b = t / a.n_tokens, i = t - b * a.n_tokens;
+    const T* q = reinterpret_cast<const T*>(a.q.p) + b * a.q.bs + i * a.q.ts;
+    const T* k = reinterpret_cast<const T*>(a.k.p) + b * a.k.bs + i * a.k.ts;
+    const T* v = reinterpret_cast<const T*>(a.v.p) + b * a.v.bs + i * a.v.ts;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!on[u]) continue;
+      const T* row = (kind[u] == 0 ? q : kind[u] == 1 ? k : v) + src_off[u];
+      xa[u] = *reinterpret_cast<const Raw4<T>*>(row + oa);
+      xb[u] = *reinterpret_cast<const Raw4<T>*>(row + ob);
+    }
+  };
+
+  // pairs that this lane turns, for every token: wt * 32 + lane, and wpt * 32 on
+  constexpr int kSlots = D / 64;
+  auto first_of = [&](int p) { return INTER ? 2 * p : p < rot / 2 ? p : 2 * p; };
+  auto second_of = [&](int p) { return INTER ? 2 * p + 1 : p < rot / 2 ? p + rot / 2 : 2 * p + 1; };
+  uint64_t freq[kSlots];
+#pragma unroll
+  for (int x = 0; x < kSlots; ++x) {
+    const int p = wt * 32 + lane + x * wpt * 32;
+    freq[x] = p < rot / 2 ? turn_step(a.rope.inv_freq[p]) : 0;
+  }
+
+  int t = blockIdx.x * seats + seat;
+  const int step = gridDim.x * seats;
+  setup(0);
+  int pos = 0, slot_next = -1;
+  if (t < tokens) {
+    load(t);
+    pos = a.pos[t];
+    if (MODE != HEADS_DENSE) slot_next = a.slots[t];
+  }
   int buf = 0;
-  for (int t0 = blockIdx.x * seats; t0 < tokens; t0 += gridDim.x * seats, buf ^= 1) {
-    const int t = t0 + seat;
+  for (int t0 = blockIdx.x * seats; t0 < tokens; t0 += step, t += step, buf ^= 1) {
     const bool live = t < tokens;
-    const int b = live ? t / a.n_tokens : 0, i = live ? t - b * a.n_tokens : 0;
-    const T* qrow = reinterpret_cast<const T*>(a.q.p) + b * a.q.bs + i * a.q.ts;
-    const T* krow = reinterpret_cast<const T*>(a.k.p) + b * a.k.bs + i * a.k.ts;
-    const T* vrow = MODE == HEADS_DENSE ? nullptr : reinterpret_cast<const T*>(a.v.p) + b * a.v.bs + i * a.v.ts;
-    bool turned = false;
-    float4 ca, cb;
-    int64_t slot = -1;
-    for (int p0 = wt; p0 < passes || (p0 == wt); p0 += U * wpt) {
-      Raw4<T> xa[U], xb[U];
+    float (&tab)[2][2][D] = table[buf][seat];
+    if (live) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = (p0 + u * wpt) * RPW + sub;
-        if (live && r < n_rows) {
-          const T* src = r < a.Hq ? qrow + r * a.q.hs
-                                  : r < a.Hq + a.Hkv ? krow + (r - a.Hq) * a.k.hs : vrow + (r - a.Hq - a.Hkv) * a.v.hs;
-          xa[u] = *reinterpret_cast<const Raw4<T>*>(src + oa);
-          xb[u] = *reinterpret_cast<const Raw4<T>*>(src + ob);
+      for (int x = 0; x < kSlots; ++x) {
+        const int p = wt * 32 + lane + x * wpt * 32;
+        if (p >= D / 2) break;
+        const int ea = first_of(p), eb = second_of(p);
+        float c = 1.f, s = 0.f;
+        if (p < rot / 2) turn_of(pos, freq[x], a.rope.scale, c, s);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float* w = y == 0 ? a.rope.q_weight : a.rope.k_weight;
+          const float wa = w ? w[ea] : 1.f, wb = w ? w[eb] : 1.f;
+          tab[y][0][ea] = wa * c; tab[y][0][eb] = wb * c;
+          tab[y][1][ea] = -(wb * s); tab[y][1][eb] = wa * s;
         }
       }
-      if (!turned) {
-        turned = true;
-        if (live) {
-          const int pos = a.pos[t];
-          for (int p = wt * 32 + lane; p < rot / 2; p += wpt * 32) {
-            float2 cs;
-            turn_of(pos, a.rope.inv_freq[p], a.rope.scale, cs.x, cs.y);
-            turns[buf][seat][p] = cs;
-          }
-          if (MODE == HEADS_STEP) {
-            const int s = a.slots[t];
-            if (s >= 0) {
-              if ((s >> a.pg.page_shift) < a.pg.n_pages) slot = s;
-              else if (lane == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
-            }
-          }
-        }
-        __syncthreads();
-        ca = pa < rot / 2 ? *reinterpret_cast<const float4*>(&turns[buf][seat][pa]) : make_float4(1.f, 0.f, 1.f, 0.f);
-        cb = pb < rot / 2 ? *reinterpret_cast<const float4*>(&turns[buf][seat][pb]) : make_float4(1.f, 0.f, 1.f, 0.f);
+    }
+    __syncthreads();
+    const int slot = slot_next;
+    bool keep = MODE != HEADS_DENSE && live && slot >= 0;
+    if (keep && (slot >> a.pg.page_shift) >= a.pg.n_pages) {
+      keep = false;
+      if (lane == 0 && wt == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
+    }
+    const int64_t page_base = ((static_cast<int64_t>(slot >> a.pg.page_shift) * a.pg.Hkv * 2) << a.pg.page_shift) +
+                              (slot & ((1 << a.pg.page_shift) - 1));
+    const int b = t / a.n_tokens, i = t - b * a.n_tokens;
+    T* const qo = reinterpret_cast<T*>(a.qo.p) + b * a.qo.bs + i * a.qo.ts;
+    T* const ko = reinterpret_cast<T*>(a.ko.p) + b * a.ko.bs + i * a.ko.ts;
+
+    for (int grp = 0; grp < groups; ++grp) {
+      if (groups > 1) {
+        setup(grp);
+        if (live && grp > 0) load(t);
       }
+      Raw4<T> ya[U], yb[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) { ya[u] = xa[u]; yb[u] = xb[u]; }
+      if (grp == groups - 1) {       // the next token's first rows
+        const int tn = t + step;
+        if (tn < tokens) {
+          if (groups == 1) load(tn);
+          pos = a.pos[tn];
+          if (MODE != HEADS_DENSE) slot_next = a.slots[tn];
+        }
+      }
+      int held = -1;                 // kind whose factors are in wc, ws
+      float wc[8], ws[8];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int r = (p0 + u * wpt) * RPW + sub;
-        if ((p0 + u * wpt) * RPW >= n_rows) break;
-        const int kind = r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;    // query, key, value
-        const int h = kind == 0 ? r : kind == 1 ? r - a.Hq : r - a.Hq - a.Hkv;
-        const bool on = live && r < n_rows;
+        if (kind[u] == 3) break;     // the same for the whole warp
         float y[8];
-        float ss = 0.f;
-        if (on) {
-          unpack4(xa[u], y);
-          unpack4(xb[u], y + 4);
+        if (on[u]) {
+          unpack4(ya[u], y);
+          unpack4(yb[u], y + 4);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = 0.f;
         }
-        if (on && kind < 2) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-        }
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (kind < 2 && on) {
-          const float* w = kind == 0 ? a.rope.q_weight : a.rope.k_weight;
-          if (w != nullptr) {
-            const float rn = rsqrtf(ss * (1.f / D) + a.rope.eps);
-            float wv[8];
-            load4<float>(w + oa, wv);
-            load4<float>(w + ob, wv + 4);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = y[e] * rn * wv[e];
+        if (kind[u] < 2) {
+          if (held != kind[u]) {
+            held = kind[u];
+            load4<float>(&tab[held][0][oa], wc);
+            load4<float>(&tab[held][0][ob], wc + 4);
+            load4<float>(&tab[held][1][oa], ws);
+            load4<float>(&tab[held][1][ob], ws + 4);
           }
-          auto turn = [](float& p, float& q, float c, float s) {
-            const float p0 = p, q0 = q;
-            p = p0 * c - q0 * s;
-            q = q0 * c + p0 * s;
-          };
-          if (inter) {
-            turn(y[0], y[1], ca.x, ca.y); turn(y[2], y[3], ca.z, ca.w);
-            turn(y[4], y[5], cb.x, cb.y); turn(y[6], y[7], cb.z, cb.w);
-          } else {
-            turn(y[0], y[4], ca.x, ca.y); turn(y[1], y[5], ca.z, ca.w);
-            turn(y[2], y[6], cb.x, cb.y); turn(y[3], y[7], cb.z, cb.w);
-          }
-        }
-        if (on && (kind == 0 || MODE == HEADS_DENSE)) {
-          const RowsView& dst = kind == 0 ? a.qo : a.ko;
-          T* row = reinterpret_cast<T*>(dst.p) + b * dst.bs + i * dst.ts + h * dst.hs;
-          store4<T>(row + oa, y);
-          store4<T>(row + ob, y + 4);
-        }
-        if (MODE == HEADS_STEP) {
-          const bool keep = on && kind > 0 && slot >= 0;
-          const int64_t at = keep ? page_row(a.pg, slot, h, kind - 1) : 0;
-          if (E4M3) {
-            float m = 0.f;
-            if (keep) {
+          float rn = 1.f;
+          if (held == 0 ? q_norm : k_norm) {
+            float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(y[e]));
+            for (int e = 0; e < 8; e += 2) {
+              const float2 v = make_float2(y[e], y[e + 1]);
+              s2 = ffma2(v, v, s2);
             }
+            float ss = s2.x + s2.y;
 #pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (keep) {
-              const float scale = scale_of(m);
+            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            rn = rsqrtf(fmaf(ss, 1.f / D, a.rope.eps));
+          }
+          float z[8];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const float2 v = make_float2(y[e], y[e + 1]);
+            const float2 w = INTER ? make_float2(y[e + 1], y[e]) : make_float2(y[e ^ 4], y[(e ^ 4) + 1]);
+            float2 r = __fmul2_rn(w, make_float2(ws[e], ws[e + 1]));
+            r = ffma2(v, make_float2(wc[e], wc[e + 1]), r);
+            r = __fmul2_rn(r, make_float2(rn, rn));
+            z[e] = r.x; z[e + 1] = r.y;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = z[e];
+        }
+        if (kind[u] == 0 || MODE == HEADS_DENSE) {
+          if (live && on[u]) {
+            T* row = (kind[u] == 0 ? qo : ko) + dst_off[u];
+            store4<T>(row + oa, y);
+            store4<T>(row + ob, y + 4);
+          }
+          continue;
+        }
+        if constexpr (MODE != HEADS_DENSE) {
+          const int64_t at = page_base + page_off[u];
+          if constexpr (E4M3) {
+            uint32_t m = top_bits(y);
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (keep && on[u]) {
+              const float scale = scale_of(__uint_as_float(m));
               quotients(y, scale);
-              *reinterpret_cast<uint32_t*>(a.pg.pages + at * D + oa) = to_e4m3x4(y);
-              *reinterpret_cast<uint32_t*>(a.pg.pages + at * D + ob) = to_e4m3x4(y + 4);
+              uint8_t* row = a.pg.pages + at * D;
+              *reinterpret_cast<uint32_t*>(row + oa) = to_e4m3x4(y);
+              *reinterpret_cast<uint32_t*>(row + ob) = to_e4m3x4(y + 4);
               if (l == 0) a.pg.scales[at] = scale;
             }
-          } else if (keep) {
+          } else if (keep && on[u]) {
             T* row = reinterpret_cast<T*>(a.pg.pages) + at * D;
             store4<T>(row + oa, y);
             store4<T>(row + ob, y + 4);
@@ -249,41 +323,42 @@ __global__ void __launch_bounds__(kThreads, 3) heads_kernel(const __grid_constan
         }
       }
     }
+    if (groups > 1) {
+      setup(0);
+      if (t + step < tokens) load(t + step);
+    }
   }
 }
 
 // Eight consecutive elements as they lie in memory.
 template <typename T> struct Raw8;
-template <> struct Raw8<float> { float4 a, b; };
-template <> struct Raw8<__nv_bfloat16> { uint4 a; };
-__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float* x) { unpack16(r.a, x, __nv_bfloat16()); }
-__device__ __forceinline__ void unpack8(const Raw8<float>& r, float* x) {
-  x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
-  x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
-}
+template <> struct __align__(16) Raw8<float> { float4 a, b; };
+template <> struct __align__(16) Raw8<__nv_bfloat16> { uint4 a; };
 
-// Keys and values of new tokens into pages.  Bound by HBM.  A warp takes `chunk`
-// passes of one token, RPW rows each, with U rows per lane on their way at a time.
+// Keys and values of new tokens into pages.  Bound by HBM.  A warp takes one
+// token's keys or values (blockIdx.y: which, and which `chunk` of their
+// passes), RPW rows a pass, U rows per lane on their way at a time.
 template <typename T, int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ HeadsArgs a, int passes, int chunk) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
-  const int nch = (passes + chunk - 1) / chunk;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
-  const int64_t t = item / nch;
-  if (t >= static_cast<int64_t>(a.batch) * a.n_tokens) return;
-  const int p_beg = static_cast<int>(item - t * nch) * chunk, p_end = min(passes, p_beg + chunk);
-  const int b = static_cast<int>(t / a.n_tokens), i = static_cast<int>(t - static_cast<int64_t>(b) * a.n_tokens);
-  const T* krow = reinterpret_cast<const T*>(a.k.p) + b * a.k.bs + i * a.k.ts + 8 * l;
-  const T* vrow = reinterpret_cast<const T*>(a.v.p) + b * a.v.bs + i * a.v.ts + 8 * l;
+  const int t = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  if (t >= a.batch * a.n_tokens) return;
+  const int kv = blockIdx.y & 1, p_beg = (blockIdx.y >> 1) * chunk, p_end = min(passes, p_beg + chunk);
+  const RowsView& src = kv ? a.v : a.k;
+  const int b = a.batch == 1 ? 0 : t / a.n_tokens, i = t - b * a.n_tokens;
+  int h = p_beg * RPW + sub;
+  const T* row = reinterpret_cast<const T*>(src.p) + b * src.bs + i * src.ts + h * src.hs + 8 * l;
+  const int64_t hop = RPW * src.hs;
   const int s = a.slots[t];
+  const int64_t at0 = ((static_cast<int64_t>(s >> a.pg.page_shift) * a.pg.Hkv * 2 + kv) << a.pg.page_shift) +
+                      (s & ((1 << a.pg.page_shift) - 1));
   for (int p0 = p_beg; p0 < p_end; p0 += U) {
     Raw8<T> x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int r = (p0 + u) * RPW + sub;
-      if (p0 + u < p_end && r < 2 * a.Hkv)
-        x[u] = *reinterpret_cast<const Raw8<T>*>(r < a.Hkv ? krow + r * a.k.hs : vrow + (r - a.Hkv) * a.v.hs);
+      if (p0 + u < p_end && h + u * RPW < a.Hkv) x[u] = *reinterpret_cast<const Raw8<T>*>(row);
+      row += hop;
     }
     if (s < 0) return;
     if ((s >> a.pg.page_shift) >= a.pg.n_pages) {
@@ -293,22 +368,19 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (p0 + u >= p_end) break;
-      const int r = (p0 + u) * RPW + sub;
-      const bool on = r < 2 * a.Hkv;
-      const int kv = r < a.Hkv ? 0 : 1;
-      const int64_t at = on ? page_row(a.pg, s, r - kv * a.Hkv, kv) : 0;
+      const bool on = h + u * RPW < a.Hkv;
+      const int64_t at = at0 + (static_cast<int64_t>(2 * (h + u * RPW)) << a.pg.page_shift);
       if constexpr (E4M3) {
-        float y[8];
-        float m = 0.f;
-        if (on) {
-          unpack8(x[u], y);
+        // magnitudes in pairs: unsigned order of their bits, as top_bits
+        const uint4 w = x[u].a;
+        uint32_t m2 = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+        if (!on) m2 = 0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(y[e]));
-        }
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = LPR / 2; o > 0; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
         if (on) {
-          const float scale = scale_of(m);
+          const float scale = scale_of(__uint_as_float(max(m2 & 0xffff0000u, m2 << 16)));
+          float y[8];
+          unpack16(w, y, __nv_bfloat16());
           quotients(y, scale);
           *reinterpret_cast<uint2*>(a.pg.pages + at * D + 8 * l) = make_uint2(to_e4m3x4(y), to_e4m3x4(y + 4));
           if (l == 0) a.pg.scales[at] = scale;
@@ -317,6 +389,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         *reinterpret_cast<Raw8<T>*>(reinterpret_cast<T*>(a.pg.pages) + at * D + 8 * l) = x[u];
       }
     }
+    h += U * RPW;
   }
 }
 
@@ -374,27 +447,41 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
 }
 
 template <typename T, int D, bool E4M3>
-int heads_t(const HeadsArgs& a, int mode, int num_sms, cudaStream_t st) {
-  const int rows = (mode == HEADS_APPEND ? 0 : a.Hq) + a.Hkv * (mode == HEADS_DENSE ? 1 : 2);
-  const int rpw = 32 / (D / 8);
-  const int passes = (rows + rpw - 1) / rpw;
-  const int64_t tokens = static_cast<int64_t>(a.batch) * a.n_tokens;
-  if (mode == HEADS_APPEND) {
-    const int chunk = tokens >= 4 * num_sms ? passes : 1;
-    const int64_t warps = tokens * ((passes + chunk - 1) / chunk);
-    const int64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    append_kernel<T, D, E4M3><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, passes, chunk);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
-  }
-  int shift = 0;      // warps per token: about three passes each
-  while (shift < 3 && (passes >> shift) > 3) ++shift;
-  const int seats = (kThreads / 32) >> shift;
-  const int64_t grid = (tokens + seats - 1) / seats;
-  if (mode == HEADS_DENSE)
-    heads_kernel<T, D, false, HEADS_DENSE><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, passes, shift);
-  else
-    heads_kernel<T, D, E4M3, HEADS_STEP><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a, passes, shift);
+int append_t(const HeadsArgs& a, int num_sms, cudaStream_t st) {
+  constexpr int RPW = 32 / (D / 8), W = kThreads / 32;
+  const int passes = (a.Hkv + RPW - 1) / RPW, tokens = a.batch * a.n_tokens;
+  // few tokens: one pass per warp, the shortest way through
+  const int chunk = static_cast<int64_t>(tokens) * passes < 16 * num_sms ? 1 : passes;
+  const dim3 grid((tokens + W - 1) / W, 2 * ((passes + chunk - 1) / chunk));
+  append_kernel<T, D, E4M3><<<grid, kThreads, 0, st>>>(a, passes, chunk);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <typename T, int D, bool E4M3, int MODE>
+int new_heads_t(const HeadsArgs& a, int num_sms, cudaStream_t st) {
+  constexpr int RPW = 32 / (D / 8);
+  const int q_passes = (a.Hq + RPW - 1) / RPW, kv_passes = (a.Hkv + RPW - 1) / RPW;
+  const int passes = q_passes + kv_passes * (MODE == HEADS_DENSE ? 1 : 2);
+  const int64_t tokens = static_cast<int64_t>(a.batch) * a.n_tokens;
+  // Warps per token: with few tokens one pass each, for the shortest way
+  // through; with many, up to four rows of a lane on their way at once.
+  const int most = tokens * passes < 16 * num_sms ? 1 : 4;
+  int shift = 0;
+  while (shift < 3 && (passes >> shift) > most) ++shift;
+  const int seats = (kThreads / 32) >> shift;
+  int64_t grid = (tokens + seats - 1) / seats;
+  if (grid > 2 * num_sms) grid = 2 * num_sms;      // two CTAs stay on each SM and walk the tokens
+  const unsigned n = static_cast<unsigned>(grid);
+  if (a.rope.interleaved) heads_kernel<T, D, E4M3, MODE, true><<<n, kThreads, 0, st>>>(a, q_passes, kv_passes, shift);
+  else heads_kernel<T, D, E4M3, MODE, false><<<n, kThreads, 0, st>>>(a, q_passes, kv_passes, shift);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <typename T, int D, bool E4M3>
+int heads_t(const HeadsArgs& a, int mode, int num_sms, cudaStream_t st) {
+  if (mode == HEADS_DENSE) return new_heads_t<T, D, false, HEADS_DENSE>(a, num_sms, st);
+  if (mode == HEADS_APPEND) return append_t<T, D, E4M3>(a, num_sms, st);
+  return new_heads_t<T, D, E4M3, HEADS_STEP>(a, num_sms, st);
 }
 
 template <typename T, int D, bool E4M3>
