@@ -1,11 +1,11 @@
 // Paged cache: norm and rotation of new tokens' heads, the write into pages
 // (as they are, or e4m3 with one scale per row) and the read back.
 //
-// All are one pass over rows of d elements.  A row is held by d / 8 lanes with
-// eight elements each, as two groups of four: element groups oa and ob.
+// All are one pass over rows of d elements.
 #include "kvpop_paged.cuh"
 
 #include <cuda_fp8.h>
+#include <type_traits>
 
 namespace kvpop {
 namespace {
@@ -22,17 +22,6 @@ template <> __device__ __forceinline__ void load4<float>(const float* p, float* 
 template <> __device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float* x) {
   const uint2 r = *reinterpret_cast<const uint2*>(p);
   const float2 lo = bf2_to_f2(r.x), hi = bf2_to_f2(r.y);
-  x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
-}
-// The same held as they are loaded, for rows that wait their turn.
-template <typename T> struct Raw4;
-template <> struct Raw4<float> { float4 v; };
-template <> struct Raw4<__nv_bfloat16> { uint2 v; };
-__device__ __forceinline__ void unpack4(const Raw4<float>& r, float* x) {
-  x[0] = r.v.x; x[1] = r.v.y; x[2] = r.v.z; x[3] = r.v.w;
-}
-__device__ __forceinline__ void unpack4(const Raw4<__nv_bfloat16>& r, float* x) {
-  const float2 lo = bf2_to_f2(r.v.x), hi = bf2_to_f2(r.v.y);
   x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
 }
 template <typename T> __device__ __forceinline__ void store4(T* p, const float* x);
@@ -67,7 +56,7 @@ __device__ __forceinline__ void turn_of(int pos, uint64_t step, float scale, flo
   s *= scale;
 }
 
-// e4m3(x / scale) of eight elements.  The quotients have to be the rounded
+// e4m3(x / scale) of N elements.  The quotients have to be the rounded
 // ones: bf16 rows often put them on the middle between two held values, and a
 // product with the reciprocal would send those to either side.  With r the
 // rounded reciprocal, q = x r is off by an ulp or so, and q + (x - q scale) r,
@@ -75,18 +64,19 @@ __device__ __forceinline__ void turn_of(int pos, uint64_t step, float scale, flo
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
 // 1990); compared with the division for every bf16 significand and 2^23 scales.
 // Below 2^-90 the remainder could underflow: those rows divide.
-__device__ __forceinline__ void quotients(float (&x)[8], float scale) {
+template <int N>
+__device__ __forceinline__ void quotients(float (&x)[N], float scale) {
   if (scale == 0.f) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    for (int e = 0; e < N; ++e) x[e] = 0.f;
   } else if (scale < 8.0779357e-28f) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = x[e] / scale;
+    for (int e = 0; e < N; ++e) x[e] = x[e] / scale;
   } else {
     const float r = 1.f / scale;
     const float2 r2 = make_float2(r, r), s2 = make_float2(-scale, -scale);
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
+    for (int e = 0; e < N; e += 2) {
       const float2 v = make_float2(x[e], x[e + 1]);
       const float2 q = __fmul2_rn(v, r2);
       const float2 y = ffma2(ffma2(q, s2, v), r2, q);
@@ -102,84 +92,172 @@ __device__ __forceinline__ float scale_of(float m) {
   return scale < 1.17549435e-38f ? 0.f : scale;                                   // subnormal: held as zeros
 }
 
-// Largest magnitude of eight elements as its bits: unsigned order is the order
-// of magnitudes, with infinities and then NaN on top.
-__device__ __forceinline__ uint32_t top_bits(const float (&x)[8]) {
+// Largest magnitude of N elements as its bits: unsigned order is the order of
+// magnitudes, with infinities and then NaN on top.
+template <int N>
+__device__ __forceinline__ uint32_t top_bits(const float (&x)[N]) {
   uint32_t m = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+  for (int e = 0; e < N; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
   return m;
+}
+
+// Eight consecutive elements as they lie in memory.
+template <typename T> struct Raw8;
+template <> struct __align__(16) Raw8<float> { float4 a, b; };
+template <> struct __align__(16) Raw8<__nv_bfloat16> { uint4 a; };
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float* x) {
+  store4<float>(p, x);
+  store4<float>(p + 4, x + 4);
+}
+
+// Where a lane's 16 elements of a row lie: groups of eight, A and B, each as two
+// groups of four.  Partners of a turn are the same places of A and B, or
+// neighbours.  WIDE: each group of eight is consecutive and 16-byte aligned.
+struct Places {
+  int a0, a1, b0, b1;
+};
+template <typename T, int D, bool INTER>
+__device__ __forceinline__ Places places_of(int l, int rot) {
+  if (INTER || rot == D) return Places{8 * l, 8 * l + 4, D / 2 + 8 * l, D / 2 + 8 * l + 4};
+  if (rot % 16 == 0) {
+    const int i = 8 * l < rot / 2 ? 8 * l : rot + 16 * (l - rot / 16);
+    const int j = 8 * l < rot / 2 ? i + rot / 2 : i + 8;
+    return Places{i, i + 4, j, j + 4};
+  }
+  // quadruples 2l and 2l + 1 of pairs, each turned or not
+  int at[2], to[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int q = 2 * l + x;
+    at[x] = 4 * q < rot / 2 ? 4 * q : rot + 8 * (q - rot / 8);
+    to[x] = 4 * q < rot / 2 ? at[x] + rot / 2 : at[x] + 4;
+  }
+  return Places{at[0], at[1], to[0], to[1]};
+}
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(dst), "l"(src), "n"(N) : "memory");
+}
+// Starts the copy of a group of eight elements into this lane's 16-byte cells,
+// which lie 512 bytes (a warp's worth) apart.
+template <typename T, bool WIDE>
+__device__ __forceinline__ void copy_group(uint32_t cell, const T* row, int i, int j) {
+  if constexpr (sizeof(T) == 4) {
+    cp_async<16>(cell, row + i);
+    cp_async<16>(cell + 512, row + j);
+  } else if constexpr (WIDE) {
+    cp_async<16>(cell, row + i);
+  } else {
+    cp_async<8>(cell, row + i);
+    cp_async<8>(cell + 8, row + j);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void read_group(const uint8_t* cell, float* x) {
+  if constexpr (sizeof(T) == 4) {
+    load4<float>(reinterpret_cast<const float*>(cell), x);
+    load4<float>(reinterpret_cast<const float*>(cell + 512), x + 4);
+  } else {
+    unpack16(*reinterpret_cast<const uint4*>(cell), x, __nv_bfloat16());
+  }
+}
+template <typename T, bool WIDE>
+__device__ __forceinline__ void store_group(T* row, int i, int j, const float* x) {
+  if constexpr (WIDE) {
+    store8(row + i, x);
+  } else {
+    store4<T>(row + i, x);
+    store4<T>(row + j, x + 4);
+  }
+}
+// Sixteen quotients as e4m3.
+template <bool WIDE>
+__device__ __forceinline__ void store_e4m3(uint8_t* row, const Places& at, const float* x) {
+  if constexpr (WIDE) {
+    *reinterpret_cast<uint2*>(row + at.a0) = make_uint2(to_e4m3x4(x), to_e4m3x4(x + 4));
+    *reinterpret_cast<uint2*>(row + at.b0) = make_uint2(to_e4m3x4(x + 8), to_e4m3x4(x + 12));
+  } else {
+    *reinterpret_cast<uint32_t*>(row + at.a0) = to_e4m3x4(x);
+    *reinterpret_cast<uint32_t*>(row + at.a1) = to_e4m3x4(x + 4);
+    *reinterpret_cast<uint32_t*>(row + at.b0) = to_e4m3x4(x + 8);
+    *reinterpret_cast<uint32_t*>(row + at.b1) = to_e4m3x4(x + 12);
+  }
 }
 
 // New tokens' heads.  HEADS_DENSE: queries and keys are normalised, turned and
 // written; HEADS_STEP: the same, but keys, and the values as they are, go into pages.
 //
-// Bound by HBM: every row is read and written once.  What stood in the way was
-// the number of instructions (265 a pass of two rows, 2.3 issued per cycle),
-// so all that does not depend on the token is done once: a warp keeps the same
-// heads for every token of its CTA (addresses, kinds), and the norm's weights
-// are multiplied into the token's cosines and sines, once per token, in shared
-// memory:  y = (x * wc + x_partner * ws) / rms.  The next token's rows are
-// loaded before the present one's are worked on.
-template <typename T, int D, bool E4M3, int MODE, bool INTER>
+// Bound by HBM: every row is read and written once.  What stands in the way is
+// the number of instructions and the bytes on their way.  So d / 16 lanes share
+// a row (a sum of squares takes three exchanges for four rows), with many
+// tokens one warp takes a whole token (position and turns once, no barrier),
+// the norm's weights are multiplied into the token's cosines and sines, in
+// shared memory:  y = (x * wc + x_partner * ws) / rms,  and rows come by
+// asynchronous copies, DEPTH passes ahead across tokens, into cells that only
+// the lane that asked for them reads, so that they need no registers and no
+// barrier.
+template <typename T, int D, bool E4M3, int MODE, bool INTER, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constant__ HeadsArgs a, int q_passes, int kv_passes, int wpt_shift) {
-  constexpr int LPR = D / 8;          // lanes per row
+  constexpr int LPR = D / 16;         // lanes per row
   constexpr int RPW = 32 / LPR;       // rows per warp and pass
-  constexpr int U = 4;                // rows of a lane on their way
-  // [buffer][token of the CTA][query, key][wc, ws][element]
-  __shared__ __align__(16) float table[2][kThreads / 32][2][2][D];
+  constexpr int kSlots = D / 64;      // pairs of a lane, at most
+  constexpr int PASS = 32 * 16 * sizeof(T);      // bytes of a pass
+  constexpr int DEPTH = sizeof(T) == 2 ? 6 : 4;
+  extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % LPR, sub = lane / LPR;
   const int wpt = 1 << wpt_shift;     // warps per token
   const int seat = warp >> wpt_shift, wt = warp & (wpt - 1), seats = (kThreads / 32) >> wpt_shift;
   const int tokens = a.batch * a.n_tokens;
-  const int rot = a.rope.rot;
   const int passes = q_passes + kv_passes * (MODE == HEADS_DENSE ? 1 : 2);
-  const int groups = (passes + U * wpt - 1) / (U * wpt);
-  // the lane's element groups [oa, oa + 4), [ob, ob + 4): partners are equal places of the two, or neighbours
-  int oa = 4 * l, ob = D / 2 + 4 * l;
-  if (!INTER && rot < D) {
-    const int j = l - rot / 8;
-    oa = j < 0 ? 4 * l : rot + 4 * j;
-    ob = j < 0 ? 4 * l + rot / 2 : rot + (D - rot) / 2 + 4 * j;
-  }
-  const bool q_norm = a.rope.q_weight != nullptr, k_norm = a.rope.k_weight != nullptr;
+  const int rot = a.rope.rot;
+  const Places at_ = places_of<T, D, INTER>(l, rot);
+  uint8_t* const ring = smem + warp * (DEPTH * PASS) + lane * 16;
+  float* const tab = reinterpret_cast<float*>(smem + (kThreads / 32) * (DEPTH * PASS)) + seat * (4 * D);   // [query, key][wc, ws][element]
 
-  // rows of a group: kind 0 query, 1 key, 2 value, 3 none
-  int kind[U], page_off[U];
-  bool on[U];
-  int64_t src_off[U], dst_off[U];
-  auto setup = [&](int grp) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int p = (grp * U + u) * wpt + wt;
-      kind[u] = p >= passes ? 3 : p < q_passes ? 0 : p < q_passes + kv_passes ? 1 : 2;
-      const int h = (kind[u] == 0 ? p : kind[u] == 1 ? p - q_passes : p - q_passes - kv_passes) * RPW + sub;
-      on[u] = kind[u] < 3 && h < (kind[u] == 0 ? a.Hq : a.Hkv);
-      src_off[u] = h * (kind[u] == 0 ? a.q.hs : kind[u] == 1 ? a.k.hs : a.v.hs);
-      dst_off[u] = h * (kind[u] == 0 ? a.qo.hs : a.ko.hs);
-      page_off[u] = (h * 2 + kind[u] - 1) << a.pg.page_shift;
-    }
+  const int step = gridDim.x * seats;
+  auto batch_of = [&](int t) { return a.batch == 1 ? 0 : t / a.n_tokens; };
+
+  // ---- copies: pass g of token pt, DEPTH passes ahead ----
+  int pt = blockIdx.x * seats + seat, pg = wt, p_cell = 0;
+  const T *pq = nullptr, *pk = nullptr, *pv = nullptr;
+  auto open = [&]() {
+    if (pt >= tokens) return;
+    const int b = batch_of(pt), i = pt - b * a.n_tokens;
+    pq = reinterpret_cast<const T*>(a.q.p) + b * a.q.bs + i * a.q.ts;
+    pk = reinterpret_cast<const T*>(a.k.p) + b * a.k.bs + i * a.k.ts;
+    if (MODE == HEADS_STEP) pv = reinterpret_cast<const T*>(a.v.p) + b * a.v.bs + i * a.v.ts;
   };
-  Raw4<T> xa[U], xb[U];
-  auto load = [&](int t) {
-    const int b = t / a.n_tokens, i = t - b * a.n_tokens;
-    const T* q = reinterpret_cast<const T*>(a.q.p) + b * a.q.bs + i * a.q.ts;
-    const T* k = reinterpret_cast<const T*>(a.k.p) + b * a.k.bs + i * a.k.ts;
-    const T* v = reinterpret_cast<const T*>(a.v.p) + b * a.v.bs + i * a.v.ts;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (!on[u]) continue;
-      const T* row = (kind[u] == 0 ? q : kind[u] == 1 ? k : v) + src_off[u];
-      xa[u] = *reinterpret_cast<const Raw4<T>*>(row + oa);
-      xb[u] = *reinterpret_cast<const Raw4<T>*>(row + ob);
+  auto ask = [&]() {
+    if (pt < tokens && pg < passes) {
+      const int kind = pg < q_passes ? 0 : pg < q_passes + kv_passes ? 1 : 2;
+      const int h = (kind == 0 ? pg : kind == 1 ? pg - q_passes : pg - q_passes - kv_passes) * RPW + sub;
+      if (h < (kind == 0 ? a.Hq : a.Hkv)) {
+        const T* row = kind == 0 ? pq + h * a.q.hs : kind == 1 ? pk + h * a.k.hs : pv + h * a.v.hs;
+        const uint32_t cell = smem_u32(ring) + p_cell * PASS;
+        copy_group<T, WIDE>(cell, row, at_.a0, at_.a1);
+        copy_group<T, WIDE>(cell + PASS / 2, row, at_.b0, at_.b1);
+      }
+      p_cell = p_cell + 1 == DEPTH ? 0 : p_cell + 1;
+      pg += wpt;
+      if (pg >= passes) {
+        pg = wt;
+        pt += step;
+        open();
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  open();
+#pragma unroll 1
+  for (int x = 0; x < DEPTH; ++x) ask();
 
   // pairs that this lane turns, for every token: wt * 32 + lane, and wpt * 32 on
-  constexpr int kSlots = D / 64;
-  auto first_of = [&](int p) { return INTER ? 2 * p : p < rot / 2 ? p : 2 * p; };
-  auto second_of = [&](int p) { return INTER ? 2 * p + 1 : p < rot / 2 ? p + rot / 2 : 2 * p + 1; };
   uint64_t freq[kSlots];
 #pragma unroll
   for (int x = 0; x < kSlots; ++x) {
@@ -187,160 +265,144 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
     freq[x] = p < rot / 2 ? turn_step(a.rope.inv_freq[p]) : 0;
   }
 
-  int t = blockIdx.x * seats + seat;
-  const int step = gridDim.x * seats;
-  setup(0);
-  int pos = 0, slot_next = -1;
-  if (t < tokens) {
-    load(t);
-    pos = a.pos[t];
-    if (MODE != HEADS_DENSE) slot_next = a.slots[t];
-  }
-  int buf = 0;
-  for (int t0 = blockIdx.x * seats; t0 < tokens; t0 += step, t += step, buf ^= 1) {
+  int cell = 0;
+#pragma unroll 1
+  for (int t0 = blockIdx.x * seats; t0 < tokens; t0 += step) {
+    const int t = t0 + seat;
     const bool live = t < tokens;
-    float (&tab)[2][2][D] = table[buf][seat];
+    int slot = -1;
     if (live) {
+      const int pos = a.pos[t];
+      if (MODE == HEADS_STEP) slot = a.slots[t];
 #pragma unroll
       for (int x = 0; x < kSlots; ++x) {
         const int p = wt * 32 + lane + x * wpt * 32;
         if (p >= D / 2) break;
-        const int ea = first_of(p), eb = second_of(p);
+        const int ea = INTER ? 2 * p : p < rot / 2 ? p : 2 * p;
+        const int eb = INTER ? 2 * p + 1 : p < rot / 2 ? p + rot / 2 : 2 * p + 1;
         float c = 1.f, s = 0.f;
         if (p < rot / 2) turn_of(pos, freq[x], a.rope.scale, c, s);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const float* w = y == 0 ? a.rope.q_weight : a.rope.k_weight;
           const float wa = w ? w[ea] : 1.f, wb = w ? w[eb] : 1.f;
-          tab[y][0][ea] = wa * c; tab[y][0][eb] = wb * c;
-          tab[y][1][ea] = -(wb * s); tab[y][1][eb] = wa * s;
+          float* to = tab + 2 * y * D;
+          to[ea] = wa * c; to[eb] = wb * c;
+          to[D + ea] = -(wb * s); to[D + eb] = wa * s;
         }
       }
     }
-    __syncthreads();
-    const int slot = slot_next;
-    bool keep = MODE != HEADS_DENSE && live && slot >= 0;
+    if (wpt_shift) __syncthreads();
+    else __syncwarp();
+    bool keep = MODE == HEADS_STEP && live && slot >= 0;
     if (keep && (slot >> a.pg.page_shift) >= a.pg.n_pages) {
       keep = false;
       if (lane == 0 && wt == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
     }
     const int64_t page_base = ((static_cast<int64_t>(slot >> a.pg.page_shift) * a.pg.Hkv * 2) << a.pg.page_shift) +
                               (slot & ((1 << a.pg.page_shift) - 1));
-    const int b = t / a.n_tokens, i = t - b * a.n_tokens;
-    T* const qo = reinterpret_cast<T*>(a.qo.p) + b * a.qo.bs + i * a.qo.ts;
-    T* const ko = reinterpret_cast<T*>(a.ko.p) + b * a.ko.bs + i * a.ko.ts;
-
-    for (int grp = 0; grp < groups; ++grp) {
-      if (groups > 1) {
-        setup(grp);
-        if (live && grp > 0) load(t);
-      }
-      Raw4<T> ya[U], yb[U];
+    if (live) {
+      const int b = batch_of(t), i = t - b * a.n_tokens;
+      T* const qo = reinterpret_cast<T*>(a.qo.p) + b * a.qo.bs + i * a.qo.ts;
+      T* const ko = reinterpret_cast<T*>(a.ko.p) + b * a.ko.bs + i * a.ko.ts;
+      int held = -1;                  // kind whose factors are in wc, ws
+      float wc[16], ws[16];
+#pragma unroll 1
+      for (int g = wt; g < passes; g += wpt) {
+        const int kind = g < q_passes ? 0 : g < q_passes + kv_passes ? 1 : 2;    // the same for the warp
+        const int h = (kind == 0 ? g : kind == 1 ? g - q_passes : g - q_passes - kv_passes) * RPW + sub;
+        const bool on = h < (kind == 0 ? a.Hq : a.Hkv);
+        asm volatile("cp.async.wait_group %0;" :: "n"(DEPTH - 1) : "memory");
+        float y[16];
+        read_group<T>(ring + cell * PASS, y);
+        read_group<T>(ring + cell * PASS + PASS / 2, y + 8);
+        cell = cell + 1 == DEPTH ? 0 : cell + 1;
+        if (kind < 2) {
+          if (held != kind) {
+            held = kind;
 #pragma unroll
-      for (int u = 0; u < U; ++u) { ya[u] = xa[u]; yb[u] = xb[u]; }
-      if (grp == groups - 1) {       // the next token's first rows
-        const int tn = t + step;
-        if (tn < tokens) {
-          if (groups == 1) load(tn);
-          pos = a.pos[tn];
-          if (MODE != HEADS_DENSE) slot_next = a.slots[tn];
-        }
-      }
-      int held = -1;                 // kind whose factors are in wc, ws
-      float wc[8], ws[8];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (kind[u] == 3) break;     // the same for the whole warp
-        float y[8];
-        if (on[u]) {
-          unpack4(ya[u], y);
-          unpack4(yb[u], y + 4);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = 0.f;
-        }
-        if (kind[u] < 2) {
-          if (held != kind[u]) {
-            held = kind[u];
-            load4<float>(&tab[held][0][oa], wc);
-            load4<float>(&tab[held][0][ob], wc + 4);
-            load4<float>(&tab[held][1][oa], ws);
-            load4<float>(&tab[held][1][ob], ws + 4);
+            for (int x = 0; x < 2; ++x) {
+              float* w = x == 0 ? wc : ws;
+              const float* from = tab + (2 * kind + x) * D;
+              load4<float>(from + at_.a0, w);
+              load4<float>(from + at_.a1, w + 4);
+              load4<float>(from + at_.b0, w + 8);
+              load4<float>(from + at_.b1, w + 12);
+            }
           }
           float rn = 1.f;
-          if (held == 0 ? q_norm : k_norm) {
-            float2 s2 = make_float2(0.f, 0.f);
+          if ((kind == 0 ? a.rope.q_weight : a.rope.k_weight) != nullptr) {
+            float2 s2 = make_float2(0.f, 0.f), s3 = s2;
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float2 v = make_float2(y[e], y[e + 1]);
+            for (int e = 0; e < 16; e += 4) {
+              const float2 v = make_float2(y[e], y[e + 1]), w = make_float2(y[e + 2], y[e + 3]);
               s2 = ffma2(v, v, s2);
+              s3 = ffma2(w, w, s3);
             }
-            float ss = s2.x + s2.y;
+            float ss = (s2.x + s2.y) + (s3.x + s3.y);
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             rn = rsqrtf(fmaf(ss, 1.f / D, a.rope.eps));
           }
-          float z[8];
+          float z[16];
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
+          for (int e = 0; e < 16; e += 2) {
             const float2 v = make_float2(y[e], y[e + 1]);
-            const float2 w = INTER ? make_float2(y[e + 1], y[e]) : make_float2(y[e ^ 4], y[(e ^ 4) + 1]);
+            const float2 w = INTER ? make_float2(y[e + 1], y[e]) : make_float2(y[e ^ 8], y[(e ^ 8) + 1]);
             float2 r = __fmul2_rn(w, make_float2(ws[e], ws[e + 1]));
             r = ffma2(v, make_float2(wc[e], wc[e + 1]), r);
             r = __fmul2_rn(r, make_float2(rn, rn));
             z[e] = r.x; z[e + 1] = r.y;
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = z[e];
+          for (int e = 0; e < 16; ++e) y[e] = z[e];
         }
-        if (kind[u] == 0 || MODE == HEADS_DENSE) {
-          if (live && on[u]) {
-            T* row = (kind[u] == 0 ? qo : ko) + dst_off[u];
-            store4<T>(row + oa, y);
-            store4<T>(row + ob, y + 4);
+        if (MODE == HEADS_DENSE || kind == 0) {
+          if (on) {
+            T* row = kind == 0 ? qo + h * a.qo.hs : ko + h * a.ko.hs;
+            store_group<T, WIDE>(row, at_.a0, at_.a1, y);
+            store_group<T, WIDE>(row, at_.b0, at_.b1, y + 8);
           }
-          continue;
-        }
-        if constexpr (MODE != HEADS_DENSE) {
-          const int64_t at = page_base + page_off[u];
+        } else {
+          const int64_t at = page_base + (static_cast<int64_t>(h * 2 + kind - 1) << a.pg.page_shift);
           if constexpr (E4M3) {
-            uint32_t m = top_bits(y);
+            uint32_t m = on ? top_bits(y) : 0u;
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (keep && on[u]) {
+            if (keep && on) {
               const float scale = scale_of(__uint_as_float(m));
               quotients(y, scale);
-              uint8_t* row = a.pg.pages + at * D;
-              *reinterpret_cast<uint32_t*>(row + oa) = to_e4m3x4(y);
-              *reinterpret_cast<uint32_t*>(row + ob) = to_e4m3x4(y + 4);
+              store_e4m3<WIDE>(a.pg.pages + at * D, at_, y);
               if (l == 0) a.pg.scales[at] = scale;
             }
-          } else if (keep && on[u]) {
+          } else if (keep && on) {
             T* row = reinterpret_cast<T*>(a.pg.pages) + at * D;
-            store4<T>(row + oa, y);
-            store4<T>(row + ob, y + 4);
+            store_group<T, WIDE>(row, at_.a0, at_.a1, y);
+            store_group<T, WIDE>(row, at_.b0, at_.b1, y + 8);
           }
         }
+        ask();
       }
     }
-    if (groups > 1) {
-      setup(0);
-      if (t + step < tokens) load(t + step);
+    // the table is written again for the next token
+    if (t0 + step < tokens) {
+      if (wpt_shift) __syncthreads();
+      else __syncwarp();
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
-
-// Eight consecutive elements as they lie in memory.
-template <typename T> struct Raw8;
-template <> struct __align__(16) Raw8<float> { float4 a, b; };
-template <> struct __align__(16) Raw8<__nv_bfloat16> { uint4 a; };
+template <typename T, int D>
+constexpr int heads_smem() { return (kThreads / 32) * ((sizeof(T) == 2 ? 6 : 4) * 32 * 16 * static_cast<int>(sizeof(T)) + 4 * D * 4); }
 
 // Keys and values of new tokens into pages.  Bound by HBM.  A warp takes one
 // token's keys or values (blockIdx.y: which, and which `chunk` of their
-// passes), RPW rows a pass, U rows per lane on their way at a time.
+// passes), RPW rows a pass, U passes on their way at a time.  Rows that are
+// only copied take d / 8 lanes (16 bytes each in bf16), rows that are
+// quantised d / 16, which halves the exchanges and reciprocals per row.
 template <typename T, int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ HeadsArgs a, int passes, int chunk) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, U = 4;
+  constexpr int LPR = E4M3 ? D / 16 : D / 8, RPW = 32 / LPR, U = E4M3 ? 2 : 4;
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
   const int t = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
   if (t >= a.batch * a.n_tokens) return;
@@ -354,10 +416,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const int64_t at0 = ((static_cast<int64_t>(s >> a.pg.page_shift) * a.pg.Hkv * 2 + kv) << a.pg.page_shift) +
                       (s & ((1 << a.pg.page_shift) - 1));
   for (int p0 = p_beg; p0 < p_end; p0 += U) {
-    Raw8<T> x[U];
+    Raw8<T> x[U], x2[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (p0 + u < p_end && h + u * RPW < a.Hkv) x[u] = *reinterpret_cast<const Raw8<T>*>(row);
+      if (p0 + u < p_end && h + u * RPW < a.Hkv) {
+        x[u] = *reinterpret_cast<const Raw8<T>*>(row);
+        if (E4M3) x2[u] = *reinterpret_cast<const Raw8<T>*>(row + D / 2);
+      }
       row += hop;
     }
     if (s < 0) return;
@@ -372,17 +437,22 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       const int64_t at = at0 + (static_cast<int64_t>(2 * (h + u * RPW)) << a.pg.page_shift);
       if constexpr (E4M3) {
         // magnitudes in pairs: unsigned order of their bits, as top_bits
-        const uint4 w = x[u].a;
-        uint32_t m2 = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+        const uint4 w = x[u].a, w2 = x2[u].a;
+        constexpr uint32_t k = 0x7fff7fffu;
+        uint32_t m2 = __vmaxu2(__vmaxu2(__vmaxu2(w.x & k, w.y & k), __vmaxu2(w.z & k, w.w & k)),
+                               __vmaxu2(__vmaxu2(w2.x & k, w2.y & k), __vmaxu2(w2.z & k, w2.w & k)));
         if (!on) m2 = 0;
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
         if (on) {
           const float scale = scale_of(__uint_as_float(max(m2 & 0xffff0000u, m2 << 16)));
-          float y[8];
+          float y[16];
           unpack16(w, y, __nv_bfloat16());
+          unpack16(w2, y + 8, __nv_bfloat16());
           quotients(y, scale);
-          *reinterpret_cast<uint2*>(a.pg.pages + at * D + 8 * l) = make_uint2(to_e4m3x4(y), to_e4m3x4(y + 4));
+          uint8_t* held = a.pg.pages + at * D + 8 * l;
+          *reinterpret_cast<uint2*>(held) = make_uint2(to_e4m3x4(y), to_e4m3x4(y + 4));
+          *reinterpret_cast<uint2*>(held + D / 2) = make_uint2(to_e4m3x4(y + 8), to_e4m3x4(y + 12));
           if (l == 0) a.pg.scales[at] = scale;
         }
       } else if (on) {
@@ -448,7 +518,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
 
 template <typename T, int D, bool E4M3>
 int append_t(const HeadsArgs& a, int num_sms, cudaStream_t st) {
-  constexpr int RPW = 32 / (D / 8), W = kThreads / 32;
+  constexpr int RPW = 32 / (E4M3 ? D / 16 : D / 8), W = kThreads / 32;
   const int passes = (a.Hkv + RPW - 1) / RPW, tokens = a.batch * a.n_tokens;
   // few tokens: one pass per warp, the shortest way through
   const int chunk = static_cast<int64_t>(tokens) * passes < 16 * num_sms ? 1 : passes;
@@ -459,21 +529,22 @@ int append_t(const HeadsArgs& a, int num_sms, cudaStream_t st) {
 
 template <typename T, int D, bool E4M3, int MODE>
 int new_heads_t(const HeadsArgs& a, int num_sms, cudaStream_t st) {
-  constexpr int RPW = 32 / (D / 8);
+  constexpr int RPW = 32 / (D / 16);
   const int q_passes = (a.Hq + RPW - 1) / RPW, kv_passes = (a.Hkv + RPW - 1) / RPW;
   const int passes = q_passes + kv_passes * (MODE == HEADS_DENSE ? 1 : 2);
   const int64_t tokens = static_cast<int64_t>(a.batch) * a.n_tokens;
-  // Warps per token: with few tokens one pass each, for the shortest way
-  // through; with many, up to four rows of a lane on their way at once.
-  const int most = tokens * passes < 16 * num_sms ? 1 : 4;
+  // Warps per token: as many as it takes to have 16 warps on each SM, up to one pass each.
   int shift = 0;
-  while (shift < 3 && (passes >> shift) > most) ++shift;
+  while (shift < 3 && (passes >> shift) > 1 && (tokens << shift) < 16 * num_sms) ++shift;
   const int seats = (kThreads / 32) >> shift;
   int64_t grid = (tokens + seats - 1) / seats;
   if (grid > 2 * num_sms) grid = 2 * num_sms;      // two CTAs stay on each SM and walk the tokens
-  const unsigned n = static_cast<unsigned>(grid);
-  if (a.rope.interleaved) heads_kernel<T, D, E4M3, MODE, true><<<n, kThreads, 0, st>>>(a, q_passes, kv_passes, shift);
-  else heads_kernel<T, D, E4M3, MODE, false><<<n, kThreads, 0, st>>>(a, q_passes, kv_passes, shift);
+  const auto kernel = a.rope.interleaved      ? heads_kernel<T, D, E4M3, MODE, true, true>
+                      : a.rope.rot % 16 == 0 ? heads_kernel<T, D, E4M3, MODE, false, true>
+                                             : heads_kernel<T, D, E4M3, MODE, false, false>;
+  constexpr int smem = heads_smem<T, D>();
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
+  kernel<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a, q_passes, kv_passes, shift);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
