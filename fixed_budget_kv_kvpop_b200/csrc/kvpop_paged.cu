@@ -253,27 +253,36 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  open();
-#pragma unroll 1
-  for (int x = 0; x < DEPTH; ++x) ask();
-
+  // positions and slots are read one token ahead, frequencies before the first copies are asked for
+  int pos_next = 0, slot_next = -1;
+  auto look = [&](int t) {
+    if (t >= tokens) return;
+    pos_next = a.pos[t];
+    if (MODE == HEADS_STEP) slot_next = a.slots[t];
+  };
+  look(pt);
   // pairs that this lane turns, for every token: wt * 32 + lane, and wpt * 32 on
+  double inv_freq[kSlots];
   uint64_t freq[kSlots];
 #pragma unroll
   for (int x = 0; x < kSlots; ++x) {
     const int p = wt * 32 + lane + x * wpt * 32;
-    freq[x] = p < rot / 2 ? turn_step(a.rope.inv_freq[p]) : 0;
+    inv_freq[x] = p < rot / 2 ? a.rope.inv_freq[p] : 0.0;
   }
+  open();
+#pragma unroll 1
+  for (int x = 0; x < DEPTH; ++x) ask();
+#pragma unroll
+  for (int x = 0; x < kSlots; ++x) freq[x] = turn_step(inv_freq[x]);
 
   int cell = 0;
 #pragma unroll 1
   for (int t0 = blockIdx.x * seats; t0 < tokens; t0 += step) {
     const int t = t0 + seat;
     const bool live = t < tokens;
-    int slot = -1;
+    const int pos = pos_next, slot = slot_next;
+    look(t + step);
     if (live) {
-      const int pos = a.pos[t];
-      if (MODE == HEADS_STEP) slot = a.slots[t];
 #pragma unroll
       for (int x = 0; x < kSlots; ++x) {
         const int p = wt * 32 + lane + x * wpt * 32;
