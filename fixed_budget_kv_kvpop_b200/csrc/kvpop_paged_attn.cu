@@ -123,20 +123,26 @@ struct Walk {
   }
 };
 
-template <int D, bool E4M3, int GP>
+// What a warp's ring holds.  A block is NSUB pieces of KEYS keys and values;
+// a piece comes by one tensor copy (bf16, e4m3) or two plain ones (fp32).
+template <typename T, int D, bool E4M3, int GP>
 struct Geo {
-  static constexpr int ES = E4M3 ? 1 : 2;
-  static constexpr int SUB = 2 * 16 * D * ES;                // bytes of 16 keys and values
-  static constexpr int NSUB = 8192 / SUB;
-  static constexpr int KB = 16 * NSUB;                       // keys of a block (one stage)
-  static constexpr int ROWB = D * ES < 128 ? D * ES : 128;   // bytes of a row in one box
+  static constexpr bool F32 = sizeof(T) == 4;
+  static constexpr int ES = E4M3 ? 1 : static_cast<int>(sizeof(T));
+  static constexpr int KEYS = F32 && D == 128 ? 8 : 16;
+  static constexpr int SUB = 2 * KEYS * D * ES;              // bytes of a piece
+  static constexpr int STAGE = 8192;
+  static constexpr int NSUB = STAGE / SUB;
+  static constexpr int KB = KEYS * NSUB;                     // keys of a block (one stage)
+  static constexpr int ROWB = D * ES < 128 ? D * ES : 128;   // bytes of a row in one box of a tensor copy
   static constexpr int HALVES = D * ES / ROWB;
   static constexpr int SCALE = E4M3 ? NSUB * 128 : 0;        // bytes of scales of a stage
   static constexpr int MERGE = NW * GP * (D + 4) * 4;
+  static constexpr int WEIGHTS = F32 ? NW * KEYS * 16 : 0;   // fp32: weights of a piece for four heads
   static constexpr int CTA = (227 * 1024 - kCtasPerSm * 1024) / kCtasPerSm;
-  static constexpr int NST0 = (CTA - 1024 - MERGE - 512) / (NW * (8192 + SCALE + 16));
+  static constexpr int NST0 = (CTA - 1024 - MERGE - WEIGHTS - 512) / (NW * (STAGE + SCALE + 16));
   static constexpr int NST = NST0 > 8 ? 8 : NST0;
-  static constexpr int SMEM = 1024 + NW * NST * (8192 + SCALE + 16) + MERGE + 256;
+  static constexpr int SMEM = 1024 + NW * NST * (STAGE + SCALE + 16) + MERGE + WEIGHTS + 256;
 };
 
 struct AttendScratch {
@@ -145,23 +151,456 @@ struct AttendScratch {
   int32_t* ticket;   // [units], zero between launches
 };
 
+__device__ __forceinline__ void write4(__nv_bfloat16* p, const float4& o, float L, bool any) {
+  *reinterpret_cast<uint2*>(p) = any ? make_uint2(pack_bf16(o.x / L, o.y / L), pack_bf16(o.z / L, o.w / L)) : make_uint2(0u, 0u);
+}
+__device__ __forceinline__ void write4(float* p, const float4& o, float L, bool any) {
+  *reinterpret_cast<float4*>(p) = any ? make_float4(o.x / L, o.y / L, o.z / L, o.w / L) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// One warp's part of a segment for bf16 and 8-bit rows: 16 keys a piece, on
+// m16n8k16 matrix instructions.  S = Q K^T has the queries as rows (up to four
+// heads fill rows 0..3 and again 4..7), and its accumulator fragment, as
+// weights, is the B fragment of O^T += V^T P^T.  Weights go in as two bf16
+// terms (16 bits): with up to four heads the repeated rows carry the low
+// terms, so they cost nothing, else a second instruction does.  8-bit keys are
+// widened to f16 (queries then are f16 too, scaled by a power of two) and
+// values to bf16, both exactly; a key's scale multiplies its score, a value's
+// scale its weight.
 template <int D, bool E4M3, int GP>
+struct MmaPieces {
+  using Geometry = Geo<__nv_bfloat16, D, E4M3, GP>;
+  using G_ = Geometry;
+  using Elements = __nv_bfloat16;
+  static constexpr int kD = D, kGP = GP;
+  static constexpr int R = GP == 16 ? 2 : 1;      // query rows per lane
+  static constexpr int KS = D / 16;               // 16-wide steps over the head
+  uint32_t qf[KS][4];
+  float qmul[R];
+  float acc[R][KS][4];
+  float m[R], l[R];
+
+  __device__ __forceinline__ void open(const AttendArgs& a, int b, int h) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = a.G;
+    const float qscale = a.scale * kLog2e;
+    // queries as A fragments: row g (and g + 8); up to four heads fill rows 0..3 and again 4..7
+    {
+      const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(h) * G) * D;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = GP == 4 ? (g & 3) : g + 8 * r;
+        const bool on = r < R && row < G;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(qb + static_cast<int64_t>(on ? row : 0) * D);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          // bf16: elements 2t, 2t + 1 and 2t + 8, 2t + 9 of a step; 8 bits: 4t .. 4t + 3
+          qf[k][r] = on ? src[k * 8 + (E4M3 ? 2 * t : t)] : 0u;
+          qf[k][r + 2] = on ? src[k * 8 + (E4M3 ? 2 * t + 1 : t + 4)] : 0u;
+        }
+        if (r < R) qmul[r] = qscale;
+        if (E4M3 && r < R) {
+          // to f16, exactly: the row is scaled by a power of two that brings its largest magnitude to [2^13, 2^14)
+          float top = 0.f;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const float2 v = bf2_to_f2(qf[k][r + i]);
+              top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+            }
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+          e = top == 0.f || e > 127 ? 13 : e < -100 ? -100 : e;
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
+          qmul[r] = qscale * __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const float2 v = bf2_to_f2(qf[k][r + i]);
+              const __half2 hv = __floats2half2_rn(v.x * up, v.y * up);
+              qf[k][r + i] = *reinterpret_cast<const uint32_t*>(&hv);
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = -INFINITY; l[r] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[r][k][i] = 0.f;
+    }
+  }
+
+  __device__ __forceinline__ void piece(const AttendArgs& a, uint8_t* kbase, const uint8_t* scales, int key0, int lo, int n, float*, bool& cleared) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const float qscale = a.scale * kLog2e;
+    (void)qscale;
+    const uint32_t ks = smem_u32(kbase), vs = ks + G_::SUB / 2;
+    const bool part = key0 < lo || key0 + 16 > n;
+    if (part) {
+      // values of tokens that are not attended: whatever they hold, weight zero must give zero
+      const int row = lane >> 1;
+      if (key0 + row < lo || key0 + row >= n) {
+        constexpr int CH = G_::ROWB / 16;
+#pragma unroll
+        for (int hf = 0; hf < G_::HALVES; ++hf)
+#pragma unroll
+          for (int c = 0; c < CH / 2; ++c)
+            *reinterpret_cast<uint4*>(kbase + G_::SUB / 2 + hf * 16 * G_::ROWB + row * G_::ROWB + ((lane & 1) * (CH / 2) + c) * 16) =
+                make_uint4(0, 0, 0, 0);
+      }
+      cleared = true;
+      __syncwarp();
+    }
+    // address of 16-byte chunk c of row r
+    auto at = [&](uint32_t base, int r, int c) {
+      if (G_::ROWB == 128) return base + (c >> 3) * (16 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+      return base + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    };
+    // ---- scores: rows are queries, columns keys 0..7 and 8..15 ----
+    float s[2][2][4];
+#pragma unroll
+    for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[nb][c][i] = 0.f;
+    if constexpr (!E4M3) {
+#pragma unroll
+      for (int k = 0; k < KS / 2; ++k) {
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+          uint32_t f[4];
+          ldsm_x4(at(ks, nb * 8 + (lane & 7), 4 * k + (lane >> 3)), f);
+          mma_bf16_16816(s[nb][0], qf[2 * k], f[0], f[1]);
+          mma_bf16_16816(s[nb][1], qf[2 * k + 1], f[2], f[3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < KS / 4; ++k) {
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+          uint32_t f[4];
+          ldsm_x4(at(ks, nb * 8 + (lane & 7), 4 * k + (lane >> 3)), f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_f16_16816(s[nb][i & 1], qf[4 * k + i], e4m3_to_f16(static_cast<uint16_t>(f[i])),
+                          e4m3_to_f16(static_cast<uint16_t>(f[i] >> 16)));
+        }
+      }
+    }
+    float2 kf[2], vf[2];
+    if constexpr (E4M3) {
+      const float2* sp = reinterpret_cast<const float2*>(scales);
+      kf[0] = sp[t]; kf[1] = sp[4 + t]; vf[0] = sp[8 + t]; vf[1] = sp[12 + t];
+    }
+    uint32_t ph[R][2], pl[R][2];     // weights as two bf16 terms
+    float x[R][4];
+    float top[R];
+    bool raise = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float y = s[i >> 1][0][2 * r + (i & 1)] + s[i >> 1][1][2 * r + (i & 1)];
+        if constexpr (E4M3) y *= (i & 1) ? kf[i >> 1].y : kf[i >> 1].x;
+        y *= qmul[r];
+        if (a.softcap > 0.f) y = a.softcap * kLog2e * tanhf(y * (kLn2 / a.softcap));
+        if (part) {
+          const int key = key0 + (i >> 1) * 8 + 2 * t + (i & 1);
+          if (key < lo || key >= n) y = -INFINITY;
+        }
+        x[r][i] = y;
+      }
+      top[r] = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+      raise |= top[r] > m[r] + kRaise;
+    }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float y = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+        const float m1 = fmaxf(m[r], y);
+        const float c = m[r] == -INFINITY ? 0.f : ex2(m[r] - m1);
+        m[r] = m1;
+        l[r] *= c;
+        // accumulator columns 2t, 2t + 1 belong to rows 2t, 2t + 1
+        const float c0 = __shfl_sync(0xffffffffu, c, 8 * t), c1 = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          acc[r][k][0] *= c0; acc[r][k][1] *= c1;
+          acc[r][k][2] *= c0; acc[r][k][3] *= c1;
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float mu = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+      for (int nb = 0; nb < 2; ++nb) {
+        float p0 = ex2(x[r][2 * nb] - mu), p1 = ex2(x[r][2 * nb + 1] - mu);
+        l[r] += p0 + p1;
+        if constexpr (E4M3) {
+          // the value's scale goes into its weight; a masked token's scale may be anything
+          p0 = part && x[r][2 * nb] == -INFINITY ? 0.f : p0 * vf[nb].x;
+          p1 = part && x[r][2 * nb + 1] == -INFINITY ? 0.f : p1 * vf[nb].y;
+        }
+        const uint32_t hi = pack_bf16(p0, p1);
+        const float2 hf = bf2_to_f2(hi);
+        const uint32_t lo = pack_bf16(p0 - hf.x, p1 - hf.y);
+        if (GP == 4) {
+          ph[r][nb] = g < 4 ? hi : lo;     // rows 4..7 repeat the heads: they carry the low terms
+        } else {
+          ph[r][nb] = hi;
+          pl[r][nb] = lo;
+        }
+      }
+    }
+    // ---- accumulators += V^T P^T: rows are head elements, columns queries ----
+    if constexpr (!E4M3) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t f[4];
+        ldsm_x4_t(at(vs, (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), f);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          mma_bf16_16816(acc[r][k], f, ph[r][0], ph[r][1]);
+          if (GP != 4) mma_bf16_16816(acc[r][k], f, pl[r][0], pl[r][1]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < KS; k += 2) {
+        uint32_t f[4];
+        ldsm_x4_t(at(vs, (lane & 7) + (((lane >> 3) & 1) << 3), k + (lane >> 4)), f);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[4];
+          e4m3_to_bf16(f[2 * c], v[0], v[1]);
+          e4m3_to_bf16(f[2 * c + 1], v[2], v[3]);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            mma_bf16_16816(acc[r][k + c], v, ph[r][0], ph[r][1]);
+            if (GP != 4) mma_bf16_16816(acc[r][k + c], v, pl[r][0], pl[r][1]);
+          }
+        }
+      }
+    }
+  }
+
+  // Accumulators, running maxima and sums of this warp to shared memory.
+  __device__ __forceinline__ void close(float* macc, float* mml, int warp, bool any) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      const int row = g + 8 * r;
+      if (t == 0 && row < GP) {
+        float* o = mml + (warp * GP + row) * 4;
+        o[0] = m[r]; o[1] = l[r]; o[2] = any ? 1.f : 0.f;
+      }
+      if (any) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = acc[r][k][i];
+            if (GP == 4) v += __shfl_xor_sync(0xffffffffu, v, 2);    // high and low terms
+            const int q = 2 * t + (i & 1) + 8 * r;
+            const int e = k * 16 + (E4M3 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
+            if (q < GP) macc[(warp * GP + q) * D + e] = v;
+          }
+        }
+      }
+    }
+  }
+};
+
+// The same for fp32 rows, on fp32 FMAs.  Eight lanes share a key (four keys at
+// a time), each with D / 8 elements; four heads' dot products are reduced
+// together, so that each pair of lanes ends with one head's score.  The
+// weights of a piece go through shared memory, and each lane accumulates D / 32
+// elements of four heads.  More than four heads: the next four after these,
+// over the same keys, their queries read again.
+template <int D, int GP>
+struct FmaPieces {
+  using Geometry = Geo<float, D, false, GP>;
+  using G_ = Geometry;
+  using Elements = float;
+  static constexpr int kD = D, kGP = GP;
+  static constexpr int NC = GP / 4;               // groups of four heads
+  static constexpr int QV = D / 32, E = D / 32;   // float4s of a key's eighth; elements of a lane's accumulator
+  static constexpr int KEYS = G_::KEYS;
+  const float* qbase;
+  int heads;
+  float4 q[4][QV];                                // of the group in hand
+  float acc[NC][4][E];
+  float m[NC], l[NC];                             // of this lane's head of each group
+
+  __device__ __forceinline__ void load_q(int c) {
+    const int part = threadIdx.x & 7;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int v = 0; v < QV; ++v)
+        q[x][v] = 4 * c + x < heads ? *reinterpret_cast<const float4*>(qbase + static_cast<int64_t>(4 * c + x) * D + (part + 8 * v) * 4)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void open(const AttendArgs& a, int b, int h) {
+    qbase = static_cast<const float*>(a.q) + (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(h) * a.G) * D;
+    heads = a.G;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      m[c] = -INFINITY; l[c] = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[c][x][e] = 0.f;
+    }
+    if (NC == 1) load_q(0);
+  }
+
+  __device__ __forceinline__ void piece(const AttendArgs& a, uint8_t* kbase, const uint8_t*, int key0, int lo, int n, float* wbuf, bool&) {
+    const int lane = threadIdx.x & 31, part = lane & 7, kg = lane >> 3;
+    const float4* keys = reinterpret_cast<const float4*>(kbase);
+    const float* values = reinterpret_cast<const float*>(kbase + G_::SUB / 2);
+    const int k_lo = max(lo - key0, 0), k_hi = min(n - key0, KEYS);    // attended keys of the piece
+    const int head = ((part >> 2) & 1) * 2 + ((part >> 1) & 1);        // this lane's head of four
+    const float qscale = a.scale * kLog2e;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if (4 * c >= heads) break;
+      if (NC > 1) load_q(c);
+      float x[KEYS / 4];
+      float top = -INFINITY;
+#pragma unroll
+      for (int p = 0; p < KEYS / 4; ++p) {
+        const int key = 4 * p + kg;
+        float2 s[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) s[y] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < QV; ++v) {
+          const float4 k = keys[key * (D / 4) + part + 8 * v];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            s[y] = ffma2(make_float2(k.x, k.y), make_float2(q[y][v].x, q[y][v].y), s[y]);
+            s[y] = ffma2(make_float2(k.z, k.w), make_float2(q[y][v].z, q[y][v].w), s[y]);
+          }
+        }
+        // four sums over eight lanes: each exchange halves the heads a lane still adds up
+        float d[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) d[y] = s[y].x + s[y].y;
+        const bool up4 = part & 4, up2 = part & 2;
+        float e0 = (up4 ? d[2] : d[0]) + __shfl_xor_sync(0xffffffffu, up4 ? d[0] : d[2], 4);
+        float e1 = (up4 ? d[3] : d[1]) + __shfl_xor_sync(0xffffffffu, up4 ? d[1] : d[3], 4);
+        float f = (up2 ? e1 : e0) + __shfl_xor_sync(0xffffffffu, up2 ? e0 : e1, 2);
+        f += __shfl_xor_sync(0xffffffffu, f, 1);
+        f *= qscale;
+        if (a.softcap > 0.f) f = a.softcap * kLog2e * tanhf(f * (kLn2 / a.softcap));
+        x[p] = key >= k_lo && key < k_hi ? f : -INFINITY;
+        top = fmaxf(top, x[p]);
+      }
+      if (__any_sync(0xffffffffu, top > m[c] + kRaise)) {
+        float y = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+        const float m1 = fmaxf(m[c], y);
+        const float f = m[c] == -INFINITY ? 0.f : ex2(m[c] - m1);
+        m[c] = m1;
+        l[c] *= f;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const float fz = __shfl_sync(0xffffffffu, f, (z >> 1) * 4 + (z & 1) * 2);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[c][z][e] *= fz;
+        }
+      }
+      const float mu = m[c] == -INFINITY ? 0.f : m[c];
+      __syncwarp();                       // the weights before these have been read
+#pragma unroll
+      for (int p = 0; p < KEYS / 4; ++p) {
+        const float w = ex2(x[p] - mu);
+        l[c] += w;
+        if (!(part & 1)) wbuf[(4 * p + kg) * 4 + head] = w;
+      }
+      __syncwarp();
+      auto add = [&](int key) {
+        const float4 w = *reinterpret_cast<const float4*>(wbuf + key * 4);
+        const float wz[4] = {w.x, w.y, w.z, w.w};
+        float v[E];
+        if constexpr (E == 4) {
+          const float4 r = *reinterpret_cast<const float4*>(values + key * D + lane * 4);
+          v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w;
+        } else {
+          const float2 r = *reinterpret_cast<const float2*>(values + key * D + lane * 2);
+          v[0] = r.x; v[1] = r.y;
+        }
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+#pragma unroll
+          for (int e = 0; e < E; e += 2) {
+            const float2 r = ffma2(make_float2(wz[z], wz[z]), make_float2(v[e], v[e + 1]), make_float2(acc[c][z][e], acc[c][z][e + 1]));
+            acc[c][z][e] = r.x; acc[c][z][e + 1] = r.y;
+          }
+      };
+      if (k_lo == 0 && k_hi == KEYS) {
+#pragma unroll
+        for (int key = 0; key < KEYS; ++key) add(key);
+      } else {
+        // values of tokens that are not attended are not touched: they may be anything
+        for (int key = k_lo; key < k_hi; ++key) add(key);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void close(float* macc, float* mml, int warp, bool any) {
+    const int lane = threadIdx.x & 31, part = lane & 7;
+    const int head = ((part >> 2) & 1) * 2 + ((part >> 1) & 1);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      float s = l[c];
+      s += __shfl_xor_sync(0xffffffffu, s, 8);
+      s += __shfl_xor_sync(0xffffffffu, s, 16);
+      if (lane < 8 && !(part & 1)) {
+        float* o = mml + (warp * GP + 4 * c + head) * 4;
+        o[0] = m[c]; o[1] = s; o[2] = any ? 1.f : 0.f;
+      }
+      if (any) {
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+#pragma unroll
+          for (int e = 0; e < E; ++e) macc[(warp * GP + 4 * c + z) * D + lane * E + e] = acc[c][z][e];
+      }
+    }
+  }
+};
+
+template <typename C>
 __global__ void __launch_bounds__(NW * 32, kCtasPerSm)
 attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendArgs a, const AttendScratch sc) {
-  using G_ = Geo<D, E4M3, GP>;
-  constexpr int KB = G_::KB, NSUB = G_::NSUB, NST = G_::NST;
-  constexpr int R = GP == 16 ? 2 : 1;      // query rows per lane
-  constexpr int KS = D / 16;               // 16-wide steps over the head
+  using G_ = typename C::Geometry;
+  using T = typename C::Elements;
+  constexpr int D = C::kD, GP = C::kGP, KB = G_::KB, NSUB = G_::NSUB, NST = G_::NST;
+  constexpr bool E4M3 = G_::SCALE > 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * NST * 8192;
-  uint8_t* sring = smem + NW * NST * 8192 + warp * NST * G_::SCALE;
-  float* macc = reinterpret_cast<float*>(smem + NW * NST * (8192 + G_::SCALE));   // [NW][GP][D]
+  uint8_t* ring = smem + warp * NST * G_::STAGE;
+  uint8_t* sring = smem + NW * NST * G_::STAGE + warp * NST * G_::SCALE;
+  float* macc = reinterpret_cast<float*>(smem + NW * NST * (G_::STAGE + G_::SCALE));   // [NW][GP][D]
   float* mml = macc + NW * GP * D;                                                // [NW][GP][4]
   uint64_t* bars = reinterpret_cast<uint64_t*>(mml + NW * GP * 4) + warp * NST;
   int32_t* live = reinterpret_cast<int32_t*>(reinterpret_cast<uint64_t*>(mml + NW * GP * 4) + NW * NST) + warp * NST;
+  float* wbuf = reinterpret_cast<float*>(smem + G_::SMEM - 1024 - 256 - G_::WEIGHTS) + warp * (G_::WEIGHTS / (4 * NW));
   __shared__ int last_flag;
 
   if (lane == 0) {
@@ -204,7 +643,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
     const Span s = span_of(a, b);
     if (s.n > 0) continue;
     for (int i = threadIdx.x; i < a.Hq * D; i += NW * 32)
-      static_cast<__nv_bfloat16*>(a.out)[static_cast<int64_t>(b) * a.Hq * D + i] = __float2bfloat16_rn(0.f);
+      static_cast<T*>(a.out)[static_cast<int64_t>(b) * a.Hq * D + i] = Elem<T>::from_f32(0.f);
     if (a.lse)
       for (int i = threadIdx.x; i < a.Hq; i += NW * 32) a.lse[static_cast<int64_t>(b) * a.Hq + i] = -INFINITY;
   }
@@ -273,8 +712,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   auto load_page = [&]() {   // lane i: the page of sub-block i of the next block
     page_next = -2;
     if (p_more && lane < NSUB) {
-      const int key = pj * KB + lane * 16;
-      if (key < p.n && key + 16 > p.lo)
+      const int key = pj * KB + lane * G_::KEYS;
+      if (key < p.n && key + G_::KEYS > p.lo)
         page_next = a.table[p.b * a.table_stride + (key >> a.pg.page_shift)];
     }
   };
@@ -291,9 +730,15 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
     }
     __syncwarp();
     if (ok) {
-      const int row = (pj * KB + lane * 16) & ((1 << a.pg.page_shift) - 1);
+      const int row = (pj * KB + lane * G_::KEYS) & ((1 << a.pg.page_shift) - 1);
       const int w5 = page_next * Hkv + p.h;
-      tma_load_5d(ring + st * 8192 + lane * G_::SUB, &map, 0, row, 0, 0, w5, &bars[st]);
+      if constexpr (G_::F32) {
+        const float* from = reinterpret_cast<const float*>(a.pg.pages) + (((static_cast<int64_t>(w5) * 2) << a.pg.page_shift) + row) * D;
+        bulk_g2s(ring + st * G_::STAGE + lane * G_::SUB, from, G_::SUB / 2, &bars[st]);
+        bulk_g2s(ring + st * G_::STAGE + lane * G_::SUB + G_::SUB / 2, from + (static_cast<int64_t>(D) << a.pg.page_shift), G_::SUB / 2, &bars[st]);
+      } else {
+        tma_load_5d(ring + st * G_::STAGE + lane * G_::SUB, &map, 0, row, 0, 0, w5, &bars[st]);
+      }
       if (E4M3) {
         const float* s0 = a.pg.scales + ((static_cast<int64_t>(w5) * 2) << a.pg.page_shift) + row;
         bulk_g2s(sring + st * G_::SCALE + lane * 128, s0, 64, &bars[st]);
@@ -312,65 +757,10 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
 
   // ---- segments ----
   int seq_c = 0;
-  const float qscale = a.scale * kLog2e;
   while (more) {
-    // queries as A fragments: row g (and g + 8); up to four heads fill rows 0..3 and again 4..7
-    uint32_t qf[KS][4];
-    float qmul[R];
-    {
-      const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(w.b) * a.Hq + static_cast<int64_t>(w.h) * G) * D;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = GP == 4 ? (g & 3) : g + 8 * r;
-        const bool on = r < R && row < G;
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(qb + static_cast<int64_t>(on ? row : 0) * D);
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          // bf16: elements 2t, 2t + 1 and 2t + 8, 2t + 9 of a step; 8 bits: 4t .. 4t + 3
-          qf[k][r] = on ? src[k * 8 + (E4M3 ? 2 * t : t)] : 0u;
-          qf[k][r + 2] = on ? src[k * 8 + (E4M3 ? 2 * t + 1 : t + 4)] : 0u;
-        }
-        if (r < R) qmul[r] = qscale;
-        if (E4M3 && r < R) {
-          // to f16, exactly: the row is scaled by a power of two that brings its largest magnitude to [2^13, 2^14)
-          float top = 0.f;
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              const float2 v = bf2_to_f2(qf[k][r + i]);
-              top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
-            }
-          }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-          e = top == 0.f || e > 127 ? 13 : e < -100 ? -100 : e;
-          const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
-          qmul[r] = qscale * __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              const float2 v = bf2_to_f2(qf[k][r + i]);
-              const __half2 hv = __floats2half2_rn(v.x * up, v.y * up);
-              qf[k][r + i] = *reinterpret_cast<const uint32_t*>(&hv);
-            }
-          }
-        }
-      }
-    }
-    float acc[R][KS][4];
-    float m[R], l[R];
+    C c;
+    c.open(a, w.b, w.h);
     bool any = false;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      m[r] = -INFINITY; l[r] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[r][k][i] = 0.f;
-    }
 
     for (int j = first_own(w); j < w.jend; j += NW) {
       const int st = seq_c % NST;
@@ -385,160 +775,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
       for (int sub = 0; sub < NSUB; ++sub) {
         if (!((have >> sub) & 1)) continue;
         any = true;
-        const int key0 = j * KB + sub * 16;
-        uint8_t* kbase = ring + st * 8192 + sub * G_::SUB;
-        const uint32_t ks = smem_u32(kbase), vs = ks + G_::SUB / 2;
-        const bool part = key0 < w.lo || key0 + 16 > w.n;
-        if (part) {
-          // values of tokens that are not attended: whatever they hold, weight zero must give zero
-          const int row = lane >> 1;
-          if (key0 + row < w.lo || key0 + row >= w.n) {
-            constexpr int CH = G_::ROWB / 16;
-#pragma unroll
-            for (int hf = 0; hf < G_::HALVES; ++hf)
-#pragma unroll
-              for (int c = 0; c < CH / 2; ++c)
-                *reinterpret_cast<uint4*>(kbase + G_::SUB / 2 + hf * 16 * G_::ROWB + row * G_::ROWB + ((lane & 1) * (CH / 2) + c) * 16) =
-                    make_uint4(0, 0, 0, 0);
-          }
-          cleared = true;
-          __syncwarp();
-        }
-        // address of 16-byte chunk c of row r
-        auto at = [&](uint32_t base, int r, int c) {
-          if (G_::ROWB == 128) return base + (c >> 3) * (16 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-          return base + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-        };
-        // ---- scores: rows are queries, columns keys 0..7 and 8..15 ----
-        float s[2][2][4];
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[nb][c][i] = 0.f;
-        if constexpr (!E4M3) {
-#pragma unroll
-          for (int k = 0; k < KS / 2; ++k) {
-#pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
-              uint32_t f[4];
-              ldsm_x4(at(ks, nb * 8 + (lane & 7), 4 * k + (lane >> 3)), f);
-              mma_bf16_16816(s[nb][0], qf[2 * k], f[0], f[1]);
-              mma_bf16_16816(s[nb][1], qf[2 * k + 1], f[2], f[3]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < KS / 4; ++k) {
-#pragma unroll
-            for (int nb = 0; nb < 2; ++nb) {
-              uint32_t f[4];
-              ldsm_x4(at(ks, nb * 8 + (lane & 7), 4 * k + (lane >> 3)), f);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma_f16_16816(s[nb][i & 1], qf[4 * k + i], e4m3_to_f16(static_cast<uint16_t>(f[i])),
-                              e4m3_to_f16(static_cast<uint16_t>(f[i] >> 16)));
-            }
-          }
-        }
-        float2 kf[2], vf[2];
-        if constexpr (E4M3) {
-          const float2* sp = reinterpret_cast<const float2*>(sring + st * G_::SCALE + sub * 128);
-          kf[0] = sp[t]; kf[1] = sp[4 + t]; vf[0] = sp[8 + t]; vf[1] = sp[12 + t];
-        }
-        uint32_t ph[R][2], pl[R][2];     // weights as two bf16 terms
-        float x[R][4];
-        float top[R];
-        bool raise = false;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float y = s[i >> 1][0][2 * r + (i & 1)] + s[i >> 1][1][2 * r + (i & 1)];
-            if constexpr (E4M3) y *= (i & 1) ? kf[i >> 1].y : kf[i >> 1].x;
-            y *= qmul[r];
-            if (a.softcap > 0.f) y = a.softcap * kLog2e * tanhf(y * (kLn2 / a.softcap));
-            if (part) {
-              const int key = key0 + (i >> 1) * 8 + 2 * t + (i & 1);
-              if (key < w.lo || key >= w.n) y = -INFINITY;
-            }
-            x[r][i] = y;
-          }
-          top[r] = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
-          raise |= top[r] > m[r] + kRaise;
-        }
-        if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            float y = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
-            const float m1 = fmaxf(m[r], y);
-            const float c = m[r] == -INFINITY ? 0.f : ex2(m[r] - m1);
-            m[r] = m1;
-            l[r] *= c;
-            // accumulator columns 2t, 2t + 1 belong to rows 2t, 2t + 1
-            const float c0 = __shfl_sync(0xffffffffu, c, 8 * t), c1 = __shfl_sync(0xffffffffu, c, 8 * t + 4);
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              acc[r][k][0] *= c0; acc[r][k][1] *= c1;
-              acc[r][k][2] *= c0; acc[r][k][3] *= c1;
-            }
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float mu = m[r] == -INFINITY ? 0.f : m[r];
-#pragma unroll
-          for (int nb = 0; nb < 2; ++nb) {
-            float p0 = ex2(x[r][2 * nb] - mu), p1 = ex2(x[r][2 * nb + 1] - mu);
-            l[r] += p0 + p1;
-            if constexpr (E4M3) {
-              // the value's scale goes into its weight; a masked token's scale may be anything
-              p0 = part && x[r][2 * nb] == -INFINITY ? 0.f : p0 * vf[nb].x;
-              p1 = part && x[r][2 * nb + 1] == -INFINITY ? 0.f : p1 * vf[nb].y;
-            }
-            const uint32_t hi = pack_bf16(p0, p1);
-            const float2 hf = bf2_to_f2(hi);
-            const uint32_t lo = pack_bf16(p0 - hf.x, p1 - hf.y);
-            if (GP == 4) {
-              ph[r][nb] = g < 4 ? hi : lo;     // rows 4..7 repeat the heads: they carry the low terms
-            } else {
-              ph[r][nb] = hi;
-              pl[r][nb] = lo;
-            }
-          }
-        }
-        // ---- accumulators += V^T P^T: rows are head elements, columns queries ----
-        if constexpr (!E4M3) {
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            uint32_t f[4];
-            ldsm_x4_t(at(vs, (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), f);
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              mma_bf16_16816(acc[r][k], f, ph[r][0], ph[r][1]);
-              if (GP != 4) mma_bf16_16816(acc[r][k], f, pl[r][0], pl[r][1]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < KS; k += 2) {
-            uint32_t f[4];
-            ldsm_x4_t(at(vs, (lane & 7) + (((lane >> 3) & 1) << 3), k + (lane >> 4)), f);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t v[4];
-              e4m3_to_bf16(f[2 * c], v[0], v[1]);
-              e4m3_to_bf16(f[2 * c + 1], v[2], v[3]);
-#pragma unroll
-              for (int r = 0; r < R; ++r) {
-                mma_bf16_16816(acc[r][k + c], v, ph[r][0], ph[r][1]);
-                if (GP != 4) mma_bf16_16816(acc[r][k + c], v, pl[r][0], pl[r][1]);
-              }
-            }
-          }
-        }
+        c.piece(a, ring + st * G_::STAGE + sub * G_::SUB, sring + st * G_::SCALE + sub * 128, j * KB + sub * G_::KEYS, w.lo, w.n, wbuf, cleared);
       }
       if (cleared) fence_proxy_async_smem();   // those stores come before the next copy into the stage
       __syncwarp();
@@ -549,29 +786,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
     }
 
     // ---- join the warps ----
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      const int row = g + 8 * r;
-      if (t == 0 && row < GP) {
-        float* o = mml + (warp * GP + row) * 4;
-        o[0] = m[r]; o[1] = l[r]; o[2] = any ? 1.f : 0.f;
-      }
-      if (any) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = acc[r][k][i];
-            if (GP == 4) v += __shfl_xor_sync(0xffffffffu, v, 2);    // high and low terms
-            const int q = 2 * t + (i & 1) + 8 * r;
-            const int e = k * 16 + (E4M3 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
-            if (q < GP) macc[(warp * GP + q) * D + e] = v;
-          }
-        }
-      }
-    }
+    c.close(macc, mml, warp, any);
     __syncthreads();
     const bool complete = w.j == w.jlo && w.jend == w.jhi;
     const int64_t unit = static_cast<int64_t>(w.b) * Hkv + w.h;
@@ -597,9 +812,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
         o.x = fmaf(c, v.x, o.x); o.y = fmaf(c, v.y, o.y); o.z = fmaf(c, v.z, o.z); o.w = fmaf(c, v.w, o.w);
       }
       if (complete) {
-        uint2 y = make_uint2(0u, 0u);
-        if (seen > 0.f) y = make_uint2(pack_bf16(o.x / L, o.y / L), pack_bf16(o.z / L, o.w / L));
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (orow + q) * D + e) = y;
+        write4(static_cast<T*>(a.out) + (orow + q) * D + e, o, L, seen > 0.f);
         if (a.lse && e == 0) a.lse[orow + q] = seen > 0.f ? (mu + log2f(L)) * kLn2 : -INFINITY;
       } else {
         __stcg(reinterpret_cast<float4*>(sc.acc + (static_cast<int64_t>(slot) * G + q) * D + e), o);
@@ -633,9 +846,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
             o.x = o.x * ca + v.x * cb; o.y = o.y * ca + v.y * cb;
             o.z = o.z * ca + v.z * cb; o.w = o.w * ca + v.w * cb;
           }
-          uint2 y = make_uint2(0u, 0u);
-          if (seen > 0.f) y = make_uint2(pack_bf16(o.x / L, o.y / L), pack_bf16(o.z / L, o.w / L));
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (orow + q) * D + e) = y;
+          write4(static_cast<T*>(a.out) + (orow + q) * D + e, o, L, seen > 0.f);
           if (a.lse && e == 0) a.lse[orow + q] = seen > 0.f ? ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2 : -INFINITY;
         }
       }
@@ -648,68 +859,6 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
     for (; seq_c < seq_p; ++seq_c) mbar_wait(&bars[seq_c % NST], (seq_c / NST) & 1);
 }
 
-// fp32 rows: one block per (sequence, query head); each warp walks every fourth
-// key with a running maximum and sum, and the warps are joined at the end.
-template <int D>
-__global__ void __launch_bounds__(NW * 32) attend_f32_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float sm_acc[NW][D], sm_m[NW], sm_l[NW];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int hq = blockIdx.x, b = blockIdx.y, h = hq / a.G;
-  const Span sp = span_of(a, b);
-  if (sp.n != a.lens[b] && threadIdx.x == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
-  const int64_t qrow = static_cast<int64_t>(b) * a.Hq + hq;
-  const float* pages = reinterpret_cast<const float*>(a.pg.pages);
-  float q[E], acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = static_cast<const float*>(a.q)[qrow * D + lane * E + e];
-    acc[e] = 0.f;
-  }
-  float m = -INFINITY, sum = 0.f;
-  bool any = false;
-  for (int i = sp.lo + warp; i < sp.n; i += NW) {
-    const int page = a.table[b * a.table_stride + (i >> a.pg.page_shift)];
-    if (page < 0 || page >= a.pg.n_pages) {
-      if (lane == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
-      continue;
-    }
-    any = true;
-    const int64_t krow = (((static_cast<int64_t>(page) * a.pg.Hkv + h) * 2) << a.pg.page_shift) +
-                         (i & ((1 << a.pg.page_shift) - 1));
-    const int64_t vrow = krow + (1 << a.pg.page_shift);
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], pages[krow * D + lane * E + e], s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= a.scale;
-    if (a.softcap > 0.f) s = a.softcap * tanhf(s / a.softcap);
-    const float m1 = fmaxf(m, s);
-    const float mu = m1 == -INFINITY ? 0.f : m1;
-    const float c = expf(m - mu), p = expf(s - mu);
-    sum = sum * c + p;
-    m = m1;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(p, pages[vrow * D + lane * E + e], acc[e] * c);
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) sm_acc[warp][lane * E + e] = acc[e];
-  if (lane == 0) { sm_m[warp] = m; sm_l[warp] = sum; }
-  any = __syncthreads_or(any);
-  float M = -INFINITY;
-  for (int w = 0; w < NW; ++w) M = fmaxf(M, sm_m[w]);
-  const float Mu = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
-  for (int w = 0; w < NW; ++w) L += sm_l[w] * expf(sm_m[w] - Mu);
-  for (int e = threadIdx.x; e < D; e += NW * 32) {
-    float o = 0.f;
-    for (int w = 0; w < NW; ++w) o += sm_acc[w][e] * expf(sm_m[w] - Mu);
-    static_cast<float*>(a.out)[qrow * D + e] = any ? o / L : 0.f;
-  }
-  if (threadIdx.x == 0 && a.lse) a.lse[qrow] = any ? Mu + logf(L) : -INFINITY;
-}
-
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   void* fn = nullptr;
   cudaDriverEntryPointQueryResult q;
@@ -719,11 +868,20 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
 }
 
-// Calls f with the kernel of (d, 8 bits, heads per KV head) and its shared memory.
+// Calls f with the kernel of (dtype, d, 8 bits, heads per KV head) and its shared memory.
 template <typename F>
-int with_kernel(int d, bool e8, int G, F f) {
+int with_kernel(int dtype, int d, bool e8, int G, F f) {
+#define KVPOP_ATTEND_F32(DD, PP) \
+  if (d == DD && G <= PP) return f(attend_kernel<FmaPieces<DD, PP>>, FmaPieces<DD, PP>::Geometry::SMEM);
+  if (dtype == KVPOP_DTYPE_F32) {
+    if (e8) return -2;
+    KVPOP_ATTEND_F32(128, 4) KVPOP_ATTEND_F32(128, 8) KVPOP_ATTEND_F32(128, 16)
+    KVPOP_ATTEND_F32(64, 4) KVPOP_ATTEND_F32(64, 8) KVPOP_ATTEND_F32(64, 16)
+    return -2;
+  }
+#undef KVPOP_ATTEND_F32
 #define KVPOP_ATTEND(DD, EE, PP) \
-  if (d == DD && e8 == EE && G <= PP) return f(attend_kernel<DD, EE, PP>, Geo<DD, EE, PP>::SMEM);
+  if (d == DD && e8 == EE && G <= PP) return f(attend_kernel<MmaPieces<DD, EE, PP>>, MmaPieces<DD, EE, PP>::Geometry::SMEM);
   KVPOP_ATTEND(128, false, 4) KVPOP_ATTEND(128, false, 8) KVPOP_ATTEND(128, false, 16)
   KVPOP_ATTEND(128, true, 4) KVPOP_ATTEND(128, true, 8) KVPOP_ATTEND(128, true, 16)
   KVPOP_ATTEND(64, false, 4) KVPOP_ATTEND(64, false, 8) KVPOP_ATTEND(64, false, 16)
@@ -757,8 +915,7 @@ int make_attend_map(CUtensorMap* map, void* pages, int dtype, int d, bool e8, in
 }
 
 int prepare_attend(int dtype, int d, bool e8, int G) {
-  if (dtype != KVPOP_DTYPE_BF16) return 0;
-  return with_kernel(d, e8, G, [](auto kernel, int smem) {
+  return with_kernel(dtype, d, e8, G, [](auto kernel, int smem) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess ? 0 : -1;
   });
 }
@@ -766,18 +923,12 @@ int prepare_attend(int dtype, int d, bool e8, int G) {
 int launch_attend(const CUtensorMap& map, const AttendArgs& a, void* scratch, int dtype, int d, int num_sms,
                   cudaStream_t st) {
   const bool e8 = a.pg.scales != nullptr;
-  if (dtype == KVPOP_DTYPE_F32) {
-    if (e8 || (d != 64 && d != 128)) return -2;
-    if (d == 128) attend_f32_kernel<128><<<dim3(a.Hq, a.batch), NW * 32, 0, st>>>(a);
-    else attend_f32_kernel<64><<<dim3(a.Hq, a.batch), NW * 32, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
-  }
   AttendScratch sc;
   sc.acc = static_cast<float*>(scratch);
   sc.ml = sc.acc + static_cast<size_t>(kAttendRanges) * 2 * a.G * d;
   sc.ticket = reinterpret_cast<int32_t*>(sc.ml + static_cast<size_t>(kAttendRanges) * 2 * a.G * 4);
   const int grid = kCtasPerSm * num_sms < kAttendRanges ? kCtasPerSm * num_sms : kAttendRanges;
-  return with_kernel(d, e8, a.G, [&](auto kernel, int smem) {
+  return with_kernel(dtype, d, e8, a.G, [&](auto kernel, int smem) {
     kernel<<<grid, NW * 32, smem, st>>>(map, a, sc);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
   });
