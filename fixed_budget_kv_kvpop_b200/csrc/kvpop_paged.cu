@@ -472,29 +472,17 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   }
 }
 
-// Four held elements as fp32.
-template <typename T, bool E4M3>
-__device__ __forceinline__ void held4(const PagedLayer& pg, int64_t row, int D, int e0, float scale, float* x) {
-  if (E4M3) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(pg.pages + row * D + e0);
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * p)), __NV_E4M3);
-      const float2 f = __half22float2(__half2(h));
-      x[2 * p] = f.x * scale;
-      x[2 * p + 1] = f.y * scale;
-    }
-  } else {
-    load4<T>(reinterpret_cast<const T*>(pg.pages) + row * D + e0, x);
-  }
-}
-
+// Rows of sequences back out of their pages.  Bound by HBM.  A block takes
+// kGatherTokens tokens of one sequence and head, keys or values: they lie one
+// after another in their pages.  A lane moves 16 bytes of held elements, and
+// all rows of a lane are on their way before the first is converted.
 constexpr int kGatherTokens = 64;
 
 template <typename T, int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ GatherArgs a) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, l = lane % LPR;
+  constexpr int PER = 16 / (E4M3 ? 1 : static_cast<int>(sizeof(T)));    // elements per lane
+  constexpr int LPR = D / PER, STEP = kThreads / LPR, U = (kGatherTokens + STEP - 1) / STEP;
+  const int l = threadIdx.x % LPR;
   const int b = blockIdx.z, h = blockIdx.y >> 1, kv = blockIdx.y & 1;
   int n = a.lens[b];
   const int64_t cap = min(static_cast<int64_t>(a.n_tokens), static_cast<int64_t>(a.width) << a.pg.page_shift);
@@ -503,26 +491,46 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
     n = n < 0 ? 0 : static_cast<int>(cap);
   }
   const RowsView& dst = kv ? a.v : a.k;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGatherTokens;
-  for (int j = threadIdx.x / LPR; j < kGatherTokens; j += kThreads / LPR) {
-    const int64_t i = t0 + j;
-    if (i >= n) break;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kGatherTokens + threadIdx.x / LPR;
+  uint4 held[U];
+  float scale[U];
+  bool on[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = t0 + u * STEP;
+    on[u] = false;
+    if (i >= n || u * STEP + static_cast<int>(threadIdx.x) / LPR >= kGatherTokens) continue;
     const int page = a.table[b * a.table_stride + (i >> a.pg.page_shift)];
     if (page < 0 || page >= a.pg.n_pages) {
       if (l == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
       continue;
     }
+    on[u] = true;
     const int64_t row = (((static_cast<int64_t>(page) * a.pg.Hkv + h) * 2 + kv) << a.pg.page_shift) +
                         (i & ((1 << a.pg.page_shift) - 1));
-    const float scale = E4M3 ? a.pg.scales[row] : 1.f;
-    float x[8];
-    held4<T, E4M3>(a.pg, row, D, 8 * l, scale, x);
-    held4<T, E4M3>(a.pg, row, D, 8 * l + 4, scale, x + 4);
-    T* out = reinterpret_cast<T*>(dst.p) + b * dst.bs + i * dst.ts + h * dst.hs + 8 * l;
-    store4<T>(out, x);
-    store4<T>(out + 4, x + 4);
+    held[u] = *reinterpret_cast<const uint4*>(a.pg.pages + (row * LPR + l) * 16);
+    if (E4M3) scale[u] = a.pg.scales[row];
   }
-  (void)RPW;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (!on[u]) continue;
+    T* out = reinterpret_cast<T*>(dst.p) + b * dst.bs + (t0 + u * STEP) * dst.ts + h * dst.hs + PER * l;
+    if constexpr (E4M3) {
+      const uint32_t w[4] = {held[u].x, held[u].y, held[u].z, held[u].w};
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
+        const float2 f = __half22float2(__half2(r));
+        x[2 * i] = f.x * scale[u];
+        x[2 * i + 1] = f.y * scale[u];
+      }
+      store8(out, x);
+      store8(out + 8, x + 8);
+    } else {
+      *reinterpret_cast<uint4*>(out) = held[u];
+    }
+  }
 }
 
 template <typename T, int D, bool E4M3>

@@ -14,7 +14,7 @@
 namespace kvpop {
 
 constexpr int kMaxGroup = 16;      // query heads per KV head that the attention is built for
-constexpr int kAttendRanges = 512; // most CTAs of one attention launch
+constexpr int kAttendRanges = 1024;// most CTAs of one attention launch
 
 // What a kernel needs of one layer's pages.
 struct PagedLayer {

@@ -2,16 +2,20 @@
 //
 //   s_j = scale q . k_j  (then cap tanh(s_j / cap)),  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m)
 //
-// Work split.  A unit is one (sequence, KV head); its keys are cut into blocks
-// of KB.  The blocks of all units form one sequence, cut into equal contiguous
-// ranges, one per CTA, whatever the lengths of the sequences are; each CTA finds
-// its range from the lengths on the device.  A unit that lies in several ranges
-// leaves one partial (accumulator, running maximum, sum) per CTA, and the CTA
-// that arrives last joins them in the order of the ranges, so results do not
-// depend on who is last.
+// Work split.  The keys of a sequence are cut into blocks of KB.  CTAs work in
+// groups of Hkv, one for each KV head, so that the heads of a page, which are
+// neighbours in memory, are read at the same time (64 sequences of 8192 tokens
+// take 308 us so, and 328 us when CTAs take ranges of single heads wherever
+// they lie).  The groups either take one part of one sequence each, all parts
+// as even as they come, or, where that leaves the largest part well above the
+// average, equal contiguous ranges of all sequences' blocks.  Every CTA finds
+// its range from the lengths on the device.  Where a sequence lies in several
+// ranges, each leaves a partial (accumulator, running maximum, sum), and the
+// CTA that arrives last joins them in their order, so results do not depend on
+// who is last.
 // Inside a CTA each warp has a ring of stages of its own: it copies block after
 // block into it by tensor copies (one instruction per 16 keys and values) and
-// computes on the oldest.  Warps meet once per unit, to join their sums.
+// computes on the oldest.  Warps meet once per item, to join their sums.
 #include "kvpop_paged.cuh"
 
 #include <cuda_fp16.h>
@@ -22,9 +26,25 @@ namespace kvpop {
 namespace {
 
 constexpr int NW = 4;                    // warps per CTA
-constexpr int kCtasPerSm = 2;
-constexpr int kUnitBlocks = 16;          // units of at most this many blocks are not split
-constexpr int kMinShare = 8;             // blocks of a range at least
+#ifndef KV_C4
+#define KV_C4 4
+#endif
+#ifndef KV_C8
+#define KV_C8 2
+#endif
+#ifndef KV_CE
+#define KV_CE 3
+#endif
+#ifndef KV_CF
+#define KV_CF 2
+#endif
+#ifndef KV_MIN
+#define KV_MIN 8
+#endif
+constexpr int kMinShare = KV_MIN;             // blocks of a part at least
+// Largest part that is taken for one part of one sequence per group, when equal
+// ranges would have `even` blocks: ranges cost a second item and its join.
+__host__ __device__ constexpr int64_t most_of(int64_t even) { return even + even / 5 + 16; }
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;            // a running maximum moves when a score passes it by this (in powers of two)
 
@@ -49,25 +69,21 @@ __device__ __forceinline__ void mma_f16_16816(float* c, const uint32_t* a, uint3
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+// Two e4m3 bytes -> f16 pair, exactly.
+__device__ __forceinline__ uint32_t e4m3_to_f16(uint32_t x) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(r) : "r"(x));
   return r;
 }
-
-// Four e4m3 bytes -> bytes 0, 2 and bytes 1, 3 as bf16 pairs, exactly: sign,
-// exponent and fraction are moved to their bf16 places, which gives the value
-// times 2^-120 (subnormals included), and one product puts that right.
-__device__ __forceinline__ void e4m3_to_bf16(uint32_t x, uint32_t& even, uint32_t& odd) {
-  constexpr uint32_t k2p120 = 0x7b807b80u;
-  even = mul_bf16x2(((x << 4) & 0x07f007f0u) | ((x << 8) & 0x80008000u), k2p120);
-  odd = mul_bf16x2(((x >> 4) & 0x07f007f0u) | (x & 0x80008000u), k2p120);
-}
-// Two e4m3 bytes -> f16 pair.
-__device__ __forceinline__ uint32_t e4m3_to_f16(uint16_t x) {
+__device__ __forceinline__ uint32_t e4m3_to_f16_high(uint32_t x) {
   uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n cvt.rn.f16x2.e4m3x2 %0, hi;\n}" : "=r"(r) : "r"(x));
   return r;
+}
+// (lo, hi) -> f16x2 word, round to nearest even; lo in the low half.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // Attended tokens [lo, n) of sequence b.  Lengths outside the table are cut.
@@ -81,47 +97,112 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int b) {
   return Span{a.window > 0 && n > a.window ? n - a.window : 0, n};
 }
 
-// Walks the segments of a CTA: runs of blocks of one unit, in order.
+// Blocks of sequence b.
 template <int KB>
-struct Walk {
-  int b, h;          // unit
-  int lo, n;         // its attended tokens
-  int j, jend;       // blocks [j, jend) of the segment; block x holds tokens x KB .. x KB + KB - 1
-  int jlo, jhi;      // the unit's blocks
-  int64_t left;      // blocks of the CTA's range from this segment on
-  int64_t index;     // position of the segment's first block among all blocks
+__device__ __forceinline__ int blocks_of(const AttendArgs& a, int b) {
+  const Span s = span_of(a, b);
+  return (s.n + KB - 1) / KB - s.lo / KB;
+}
 
-  __device__ __forceinline__ void unit(const AttendArgs& a) {
-    const Span s = span_of(a, b);
-    lo = s.lo; n = s.n;
-    jlo = lo / KB;
-    jhi = (n + KB - 1) / KB;
-  }
-  __device__ __forceinline__ void cut() { jend = static_cast<int>(min(static_cast<int64_t>(jhi), j + left)); }
-  // To the next segment; false at the end of the range.
-  __device__ __forceinline__ bool next(const AttendArgs& a, int unit_step) {
-    if (unit_step > 0) {            // whole units, unit_step apart
-      do {
-        const int u = b * a.pg.Hkv + h + unit_step;
-        if (u >= a.batch * a.pg.Hkv) return false;
-        b = u / a.pg.Hkv; h = u % a.pg.Hkv;
-        unit(a);
-      } while (jhi == jlo);
-      j = jlo; jend = jhi;
-      return true;
-    }
-    left -= jend - j;
-    index += jend - j;
-    if (left <= 0) return false;
-    if (++h == a.pg.Hkv) {
-      h = 0;
-      do { ++b; unit(a); } while (jhi == jlo);   // blocks are left, so a unit that has some follows
-    }
-    j = jlo;
-    cut();
-    return true;
-  }
+// a / b for a >= 0, b > 0: in 32 bits where a allows, a fraction of the 64-bit division's time.
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+  if ((a >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// How the work is split; the same in every warp of the launch.
+struct Split {
+  int64_t total;     // blocks of all sequences
+  int share;         // blocks of a range
+  int groups;        // groups of CTAs
+  int nb0;           // blocks of sequence `lane`
+  bool aligned;      // one part of one sequence per group
 };
+
+// An item: blocks of one sequence and head.  Each warp keeps two in shared
+// memory, the one it computes on and the one it copies for, so that they take
+// no registers in the loops.
+struct Item {
+  int b, h;
+  int lo, n;         // the sequence's attended tokens
+  int j, jend;       // blocks [j, jend) of the item; block x holds tokens x KB .. x KB + KB - 1
+  int first, parts;  // groups that hold a part of the sequence
+  int second;        // 1: in the first of them it is not the range's first sequence
+  int left;          // blocks of the range from this item on
+  int64_t pos;       // of the item's first block among all blocks (ranges)
+};
+
+// The CTA's first or next item (the whole warp together); false at the end.
+// CTAs take one head, or with more heads than CTAs every gridDim.x-th.
+template <int KB>
+__device__ __noinline__ bool next_item(const AttendArgs& a, Item* it, const Split& sp, bool start) {
+  const int lane = threadIdx.x & 31, Hkv = a.pg.Hkv, n_cta = gridDim.x;
+  const bool many = Hkv > n_cta;
+  const int grp = many ? 0 : static_cast<int>(blockIdx.x) / Hkv;
+  int b = 0, h, part = 0, parts = 1, skip = 0, left;
+  int64_t pos = 0;
+  if (!start && it->left > it->jend - it->j) {       // the range goes on in the next sequence that has blocks
+    h = it->h;
+    left = it->left - (it->jend - it->j);
+    pos = it->pos + (it->jend - it->j);
+    b = it->b;
+    do ++b; while (blocks_of<KB>(a, b) == 0);
+  } else {
+    h = start ? (many ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) - grp * Hkv) : it->h + n_cta;
+    if (h >= Hkv || grp >= sp.groups) return false;
+    // the sequence in which the range begins
+    const int64_t target = sp.aligned ? grp : static_cast<int64_t>(grp) * sp.share;
+    int64_t before = 0;
+    for (int b0 = 0;; b0 += 32) {
+      if (b0 >= a.batch) return false;
+      int nb = 0;
+      if (b0 + lane < a.batch) nb = b0 == 0 ? sp.nb0 : blocks_of<KB>(a, b0 + lane);
+      const int own = sp.aligned ? (nb + sp.share - 1) / sp.share : nb;
+      int64_t sum = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + sum > target);
+      if (past) {
+        const int i = __ffs(past) - 1;
+        b = b0 + i;
+        parts = __shfl_sync(0xffffffffu, own, i);
+        skip = static_cast<int>(target - before - (__shfl_sync(0xffffffffu, sum, i) - parts));
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    part = skip;
+    pos = target;
+    left = static_cast<int>(min(static_cast<int64_t>(sp.share), sp.total - target));
+  }
+  __syncwarp();                      // the old item has been read
+  if (lane == 0) {
+    const Span s = span_of(a, b);
+    const int j0 = s.lo / KB, nb = (s.n + KB - 1) / KB - j0;
+    Item x;
+    x.b = b; x.h = h; x.lo = s.lo; x.n = s.n; x.pos = pos;
+    if (sp.aligned) {
+      x.j = j0 + static_cast<int>(quotient(static_cast<int64_t>(nb) * part, parts));
+      x.jend = j0 + static_cast<int>(quotient(static_cast<int64_t>(nb) * (part + 1), parts));
+      x.left = x.jend - x.j;
+      x.first = grp - part; x.parts = parts; x.second = 0;
+    } else {
+      x.j = j0 + skip;
+      x.jend = min(j0 + nb, x.j + left);
+      x.left = left;
+      const int64_t beg = pos - skip;                // of the sequence
+      x.first = static_cast<int>(quotient(beg, sp.share));
+      x.parts = static_cast<int>(quotient(beg + nb - 1, sp.share)) - x.first + 1;
+      x.second = beg != static_cast<int64_t>(x.first) * sp.share;
+    }
+    *it = x;
+  }
+  __syncwarp();
+  return true;
+}
 
 // What a warp's ring holds.  A block is NSUB pieces of KEYS keys and values;
 // a piece comes by one tensor copy (bf16, e4m3) or two plain ones (fp32).
@@ -139,15 +220,19 @@ struct Geo {
   static constexpr int SCALE = E4M3 ? NSUB * 128 : 0;        // bytes of scales of a stage
   static constexpr int MERGE = NW * GP * (D + 4) * 4;
   static constexpr int WEIGHTS = F32 ? NW * KEYS * 16 : 0;   // fp32: weights of a piece for four heads
-  static constexpr int CTA = (227 * 1024 - kCtasPerSm * 1024) / kCtasPerSm;
+  static constexpr int CTAS = GP == 16 ? 2 : GP == 8 ? KV_C8 : F32 ? KV_CF : E4M3 ? KV_CE : KV_C4;    // per SM
+  static constexpr int CTA = (228 * 1024) / CTAS - 1024;
   static constexpr int NST0 = (CTA - 1024 - MERGE - WEIGHTS - 512) / (NW * (STAGE + SCALE + 16));
   static constexpr int NST = NST0 > 8 ? 8 : NST0;
+  static_assert(NST >= 1, "a warp needs a stage");
   static constexpr int SMEM = 1024 + NW * NST * (STAGE + SCALE + 16) + MERGE + WEIGHTS + 256;
 };
 
+// A range begins in one sequence and ends in another, so a group leaves at
+// most two partials per head: that of its range's first sequence, and another.
 struct AttendScratch {
-  float* acc;        // [ranges][2][G][D]
-  float* ml;         // [ranges][2][G][4]: running maximum, sum, whether any key was seen
+  float* acc;        // [2 kAttendRanges][G][D]
+  float* ml;         // [2 kAttendRanges][G][4]: running maximum, sum, whether any key was seen
   int32_t* ticket;   // [units], zero between launches
 };
 
@@ -163,10 +248,10 @@ __device__ __forceinline__ void write4(float* p, const float4& o, float L, bool 
 // heads fill rows 0..3 and again 4..7), and its accumulator fragment, as
 // weights, is the B fragment of O^T += V^T P^T.  Weights go in as two bf16
 // terms (16 bits): with up to four heads the repeated rows carry the low
-// terms, so they cost nothing, else a second instruction does.  8-bit keys are
-// widened to f16 (queries then are f16 too, scaled by a power of two) and
-// values to bf16, both exactly; a key's scale multiplies its score, a value's
-// scale its weight.
+// terms, so they cost nothing, else a second instruction does.  8-bit rows are
+// widened to f16, exactly (queries then are f16 too, scaled by a power of two,
+// and weights are two f16 terms); a key's scale multiplies its score, a
+// value's scale its weight.
 template <int D, bool E4M3, int GP>
 struct MmaPieces {
   using Geometry = Geo<__nv_bfloat16, D, E4M3, GP>;
@@ -179,10 +264,33 @@ struct MmaPieces {
   float qmul[R];
   float acc[R][KS][4];
   float m[R], l[R];
+  // 8 bits: weights are p * scale * vmul with vmul = 64 / vref, vref a power of
+  // two above half the largest value scale so far (2^-100 at least): at most
+  // 2^15, and a weight's two f16 terms are exact to 2^-25, 2^-31 of a weight
+  // of one with the largest scale
+  float vref, vmul;
+  uint32_t kx[2], vx[4];      // this lane's offsets into a piece, for its loads of keys and of values
+
+  // Offset of 16-byte chunk c of row r in a piece's keys (or values): boxes of
+  // 128-byte (64-byte) rows, whose chunks the copy has placed at c ^ (r & 7)
+  // (c ^ (r >> 1 & 3)).
+  static __device__ __forceinline__ uint32_t place(int r, int c) {
+    if (G_::ROWB == 128) return (c >> 3) * (16 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  }
 
   __device__ __forceinline__ void open(const AttendArgs& a, int b, int h) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = a.G;
     const float qscale = a.scale * kLog2e;
+    vref = 7.8886091e-31f; vmul = 64.f / vref;      // 2^-100
+    // chunks 4 apart (keys) and 2 apart (values) differ in bits that the rows'
+    // swizzle leaves in place: the rest of a load's address is a constant
+#pragma unroll
+    for (int i = 0; i < 2; ++i) kx[i] = place(lane & 7, (4 * i + (lane >> 3)) & (G_::ROWB / 16 - 1));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      vx[i] = E4M3 ? place((lane & 7) + (((lane >> 3) & 1) << 3), (2 * i + (lane >> 4)) & (G_::ROWB / 16 - 1))
+                   : place((lane & 7) + ((lane >> 4) << 3), (2 * i + ((lane >> 3) & 1)) & (G_::ROWB / 16 - 1));
     // queries as A fragments: row g (and g + 8); up to four heads fill rows 0..3 and again 4..7
     {
       const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(b) * a.Hq + static_cast<int64_t>(h) * G) * D;
@@ -216,14 +324,12 @@ struct MmaPieces {
           const float up = __uint_as_float(static_cast<uint32_t>(127 + 13 - e) << 23);
           qmul[r] = qscale * __uint_as_float(static_cast<uint32_t>(127 - 13 + e) << 23);
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
+          for (int k = 0; k < KS; ++k)
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
               const float2 v = bf2_to_f2(qf[k][r + i]);
-              const __half2 hv = __floats2half2_rn(v.x * up, v.y * up);
-              qf[k][r + i] = *reinterpret_cast<const uint32_t*>(&hv);
+              qf[k][r + i] = pack_f16(v.x * up, v.y * up);
             }
-          }
         }
       }
     }
@@ -258,11 +364,6 @@ struct MmaPieces {
       cleared = true;
       __syncwarp();
     }
-    // address of 16-byte chunk c of row r
-    auto at = [&](uint32_t base, int r, int c) {
-      if (G_::ROWB == 128) return base + (c >> 3) * (16 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-      return base + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-    };
     // ---- scores: rows are queries, columns keys 0..7 and 8..15 ----
     float s[2][2][4];
 #pragma unroll
@@ -277,7 +378,7 @@ struct MmaPieces {
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb) {
           uint32_t f[4];
-          ldsm_x4(at(ks, nb * 8 + (lane & 7), 4 * k + (lane >> 3)), f);
+          ldsm_x4(ks + kx[k & 1] + (k >> 1) * 2048 + nb * (8 * G_::ROWB), f);
           mma_bf16_16816(s[nb][0], qf[2 * k], f[0], f[1]);
           mma_bf16_16816(s[nb][1], qf[2 * k + 1], f[2], f[3]);
         }
@@ -288,11 +389,9 @@ struct MmaPieces {
 #pragma unroll
         for (int nb = 0; nb < 2; ++nb) {
           uint32_t f[4];
-          ldsm_x4(at(ks, nb * 8 + (lane & 7), 4 * k + (lane >> 3)), f);
+          ldsm_x4(ks + kx[k & 1] + (k >> 1) * 2048 + nb * (8 * G_::ROWB), f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mma_f16_16816(s[nb][i & 1], qf[4 * k + i], e4m3_to_f16(static_cast<uint16_t>(f[i])),
-                          e4m3_to_f16(static_cast<uint16_t>(f[i] >> 16)));
+          for (int i = 0; i < 4; ++i) mma_f16_16816(s[nb][i & 1], qf[4 * k + i], e4m3_to_f16(f[i]), e4m3_to_f16_high(f[i]));
         }
       }
     }
@@ -300,6 +399,14 @@ struct MmaPieces {
     if constexpr (E4M3) {
       const float2* sp = reinterpret_cast<const float2*>(scales);
       kf[0] = sp[t]; kf[1] = sp[4 + t]; vf[0] = sp[8 + t]; vf[1] = sp[12 + t];
+      if (part) {     // scales of tokens that are not attended may be anything
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb) {
+          const int key = key0 + nb * 8 + 2 * t;
+          if (key < lo || key >= n) vf[nb].x = 0.f;
+          if (key + 1 < lo || key + 1 >= n) vf[nb].y = 0.f;
+        }
+      }
     }
     uint32_t ph[R][2], pl[R][2];     // weights as two bf16 terms
     float x[R][4];
@@ -311,18 +418,37 @@ struct MmaPieces {
       for (int i = 0; i < 4; ++i) {
         float y = s[i >> 1][0][2 * r + (i & 1)] + s[i >> 1][1][2 * r + (i & 1)];
         if constexpr (E4M3) y *= (i & 1) ? kf[i >> 1].y : kf[i >> 1].x;
-        y *= qmul[r];
-        if (a.softcap > 0.f) y = a.softcap * kLog2e * tanhf(y * (kLn2 / a.softcap));
-        if (part) {
+        x[r][i] = y * qmul[r];
+      }
+      if (a.softcap > 0.f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[r][i] = a.softcap * kLog2e * tanhf(x[r][i] * (kLn2 / a.softcap));
+      }
+      if (part) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
           const int key = key0 + (i >> 1) * 8 + 2 * t + (i & 1);
-          if (key < lo || key >= n) y = -INFINITY;
+          if (key < lo || key >= n) x[r][i] = -INFINITY;
         }
-        x[r][i] = y;
       }
       top[r] = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
       raise |= top[r] > m[r] + kRaise;
     }
+    float vtop = 0.f;
+    if constexpr (E4M3) {
+      vtop = fmaxf(fmaxf(vf[0].x, vf[0].y), fmaxf(vf[1].x, vf[1].y));
+      raise |= vtop >= 2.f * vref;
+    }
     if (__any_sync(0xffffffffu, raise)) {
+      float fall = 1.f;
+      if constexpr (E4M3) {
+        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 1));
+        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 2));
+        const float v1 = fmaxf(vref, __uint_as_float(__float_as_uint(vtop) & 0x7f800000u));
+        fall = vref / v1;
+        vref = v1;
+        vmul = 64.f / v1;
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float y = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
@@ -332,7 +458,7 @@ struct MmaPieces {
         m[r] = m1;
         l[r] *= c;
         // accumulator columns 2t, 2t + 1 belong to rows 2t, 2t + 1
-        const float c0 = __shfl_sync(0xffffffffu, c, 8 * t), c1 = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+        const float c0 = __shfl_sync(0xffffffffu, c, 8 * t) * fall, c1 = __shfl_sync(0xffffffffu, c, 8 * t + 4) * fall;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           acc[r][k][0] *= c0; acc[r][k][1] *= c1;
@@ -348,13 +474,19 @@ struct MmaPieces {
         float p0 = ex2(x[r][2 * nb] - mu), p1 = ex2(x[r][2 * nb + 1] - mu);
         l[r] += p0 + p1;
         if constexpr (E4M3) {
-          // the value's scale goes into its weight; a masked token's scale may be anything
-          p0 = part && x[r][2 * nb] == -INFINITY ? 0.f : p0 * vf[nb].x;
-          p1 = part && x[r][2 * nb + 1] == -INFINITY ? 0.f : p1 * vf[nb].y;
+          p0 *= vf[nb].x * vmul;
+          p1 *= vf[nb].y * vmul;
         }
-        const uint32_t hi = pack_bf16(p0, p1);
-        const float2 hf = bf2_to_f2(hi);
-        const uint32_t lo = pack_bf16(p0 - hf.x, p1 - hf.y);
+        uint32_t hi, lo;
+        if constexpr (E4M3) {
+          hi = pack_f16(p0, p1);
+          const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+          lo = pack_f16(p0 - hf.x, p1 - hf.y);
+        } else {
+          hi = pack_bf16(p0, p1);
+          const float2 hf = bf2_to_f2(hi);
+          lo = pack_bf16(p0 - hf.x, p1 - hf.y);
+        }
         if (GP == 4) {
           ph[r][nb] = g < 4 ? hi : lo;     // rows 4..7 repeat the heads: they carry the low terms
         } else {
@@ -368,7 +500,7 @@ struct MmaPieces {
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         uint32_t f[4];
-        ldsm_x4_t(at(vs, (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), f);
+        ldsm_x4_t(vs + vx[k & 3] + (k >> 2) * 2048, f);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           mma_bf16_16816(acc[r][k], f, ph[r][0], ph[r][1]);
@@ -379,16 +511,16 @@ struct MmaPieces {
 #pragma unroll
       for (int k = 0; k < KS; k += 2) {
         uint32_t f[4];
-        ldsm_x4_t(at(vs, (lane & 7) + (((lane >> 3) & 1) << 3), k + (lane >> 4)), f);
+        ldsm_x4_t(vs + vx[k >> 1], f);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t v[4];
-          e4m3_to_bf16(f[2 * c], v[0], v[1]);
-          e4m3_to_bf16(f[2 * c + 1], v[2], v[3]);
+          // bytes: two keys' elements 2g, 2g + 1 -> the keys' pairs of element 2g (row g) and of 2g + 1 (row g + 8)
+          const uint32_t u = __byte_perm(f[2 * c], 0, 0x3120), w = __byte_perm(f[2 * c + 1], 0, 0x3120);
+          const uint32_t v[4] = {e4m3_to_f16(u), e4m3_to_f16_high(u), e4m3_to_f16(w), e4m3_to_f16_high(w)};
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            mma_bf16_16816(acc[r][k + c], v, ph[r][0], ph[r][1]);
-            if (GP != 4) mma_bf16_16816(acc[r][k + c], v, pl[r][0], pl[r][1]);
+            mma_f16_16816(acc[r][k + c], v, ph[r][0], ph[r][1]);
+            if (GP != 4) mma_f16_16816(acc[r][k + c], v, pl[r][0], pl[r][1]);
           }
         }
       }
@@ -408,15 +540,28 @@ struct MmaPieces {
         o[0] = m[r]; o[1] = l[r]; o[2] = any ? 1.f : 0.f;
       }
       if (any) {
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][k][i] *= vref * (1.f / 64.f);
+        }
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = acc[r][k][i];
-            if (GP == 4) v += __shfl_xor_sync(0xffffffffu, v, 2);    // high and low terms
-            const int q = 2 * t + (i & 1) + 8 * r;
-            const int e = k * 16 + (E4M3 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
-            if (q < GP) macc[(warp * GP + q) * D + e] = v;
+          // element of head dimension that accumulator rows g and g + 8 hold
+          const int e0 = k * 16 + (E4M3 ? 2 * g : g), e1 = E4M3 ? e0 + 1 : e0 + 8;
+          if constexpr (GP == 4) {
+            // columns 0..3 hold the high terms' sums, 4..7 the low terms': the lanes of a pair add up one row each
+            const bool up = t & 2;
+            const float s0 = __shfl_xor_sync(0xffffffffu, up ? acc[r][k][0] : acc[r][k][2], 2);
+            const float s1 = __shfl_xor_sync(0xffffffffu, up ? acc[r][k][1] : acc[r][k][3], 2);
+            float* o = macc + (warp * GP + 2 * (t & 1)) * D + (up ? e1 : e0);
+            o[0] = (up ? acc[r][k][2] : acc[r][k][0]) + s0;
+            o[D] = (up ? acc[r][k][3] : acc[r][k][1]) + s1;
+          } else {
+            float* o = macc + (warp * GP + 2 * t + 8 * r) * D;
+            o[e0] = acc[r][k][0]; o[D + e0] = acc[r][k][1];
+            o[e1] = acc[r][k][2]; o[D + e1] = acc[r][k][3];
           }
         }
       }
@@ -585,7 +730,7 @@ struct FmaPieces {
 };
 
 template <typename C>
-__global__ void __launch_bounds__(NW * 32, kCtasPerSm)
+__global__ void __launch_bounds__(NW * 32, C::Geometry::CTAS)
 attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendArgs a, const AttendScratch sc) {
   using G_ = typename C::Geometry;
   using T = typename C::Elements;
@@ -602,114 +747,102 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   int32_t* live = reinterpret_cast<int32_t*>(reinterpret_cast<uint64_t*>(mml + NW * GP * 4) + NW * NST) + warp * NST;
   float* wbuf = reinterpret_cast<float*>(smem + G_::SMEM - 1024 - 256 - G_::WEIGHTS) + warp * (G_::WEIGHTS / (4 * NW));
   __shared__ int last_flag;
+  __shared__ Item items[NW][2];
 
   if (lane == 0) {
+    if (!G_::F32) asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map)) : "memory");
     for (int s = 0; s < NST; ++s) mbar_init(&bars[s], 1);
     mbar_fence_init();
   }
   __syncwarp();
 
-  // ---- this CTA's range ----
-  const int Hkv = a.pg.Hkv, G = a.G;
-  int64_t total = 0;
-  int longest = 0;
-  bool bad_len = false;
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const int b = b0 + lane;
-    int nb = 0;
-    if (b < a.batch) {
-      const Span s = span_of(a, b);
-      nb = (s.n + KB - 1) / KB - s.lo / KB;
-      bad_len |= a.lens[b] != s.n;
+  // ---- the split ----
+  const int Hkv = a.pg.Hkv, G = a.G, n_cta = gridDim.x;
+  Split sp;
+  {
+    int64_t total = 0;
+    int longest = 0, seqs = 0;
+    bool bad_len = false;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const int b = b0 + lane;
+      int nb = 0;
+      if (b < a.batch) {
+        nb = blocks_of<KB>(a, b);
+        bad_len |= a.lens[b] != span_of(a, b).n;
+      }
+      if (b0 == 0) sp.nb0 = nb;
+      total += nb;
+      longest = max(longest, nb);
+      seqs += __popc(__ballot_sync(0xffffffffu, nb > 0));
     }
-    total += nb;
-    longest = max(longest, nb);
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    for (int o = 16; o > 0; o >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+      longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    }
+    if (bad_len && blockIdx.x == 0 && warp == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
+    sp.total = total;
+    sp.groups = max(1, n_cta / Hkv);
+    const int64_t even = quotient(total + sp.groups - 1, sp.groups);
+    sp.share = static_cast<int>(min(max(even, static_cast<int64_t>(kMinShare)), static_cast<int64_t>(1 << 30)));
+    sp.aligned = false;
+    if (seqs > 0 && seqs <= sp.groups) {
+      // the smallest largest part with which there are no more parts than groups
+      auto fits = [&](int s) {
+        int items = 0;
+        for (int b0 = 0; b0 < a.batch; b0 += 32) {
+          int np = 0;
+          if (b0 + lane < a.batch) np = ((b0 == 0 ? sp.nb0 : blocks_of<KB>(a, b0 + lane)) + s - 1) / s;
+          items += __reduce_add_sync(0xffffffffu, min(np, sp.groups + 1));
+        }
+        return items <= sp.groups;
+      };
+      const int per = sp.groups / seqs;
+      int lo = sp.share, hi = (longest + per - 1) / per;     // hi fits: no sequence has more than `per` parts
+      if (hi <= lo || fits(lo)) {
+        hi = lo;
+      } else {
+        while (hi - lo > 1 + lo / 32) {
+          const int mid = lo + (hi - lo) / 2;
+          if (fits(mid)) hi = mid;
+          else lo = mid;
+        }
+      }
+      if (hi <= most_of(sp.share)) {
+        sp.aligned = true;
+        sp.share = hi;
+      }
+    }
   }
-  if (bad_len && blockIdx.x == 0 && warp == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
-  total *= Hkv;
-  const int n_cta = gridDim.x;
-  const bool whole = longest <= kUnitBlocks;
-  int64_t share = (total + n_cta - 1) / n_cta;
-  if (share < kMinShare) share = kMinShare;
-  const int unit_step = whole ? n_cta : 0;
 
   // sequences without a token
   for (int b = blockIdx.x; b < a.batch; b += n_cta) {
-    const Span s = span_of(a, b);
-    if (s.n > 0) continue;
+    if (span_of(a, b).n > 0) continue;
     for (int i = threadIdx.x; i < a.Hq * D; i += NW * 32)
       static_cast<T*>(a.out)[static_cast<int64_t>(b) * a.Hq * D + i] = Elem<T>::from_f32(0.f);
     if (a.lse)
       for (int i = threadIdx.x; i < a.Hq; i += NW * 32) a.lse[static_cast<int64_t>(b) * a.Hq + i] = -INFINITY;
   }
 
-  Walk<KB> w;
-  bool more = true;
-  if (whole) {
-    w.b = 0; w.h = static_cast<int>(blockIdx.x) - n_cta;
-    // unit blockIdx.x: one step from the unit before it
-    w.b = 0;
-    more = w.next(a, n_cta);
-    w.index = 0; w.left = 0;
-  } else {
-    const int64_t beg = share * blockIdx.x;
-    more = beg < total;
-    if (more) {
-      // the sequence that block `beg` lies in
-      int64_t before = 0;
-      int b0 = 0;
-      for (;; b0 += 32) {
-        const int b = b0 + lane;
-        int64_t nb = 0;
-        if (b < a.batch) {
-          const Span s = span_of(a, b);
-          nb = static_cast<int64_t>((s.n + KB - 1) / KB - s.lo / KB) * Hkv;
-        }
-        int64_t incl = nb;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
-        const unsigned past = __ballot_sync(0xffffffffu, before + incl > beg);
-        if (past) {
-          const int i = __ffs(past) - 1;
-          w.b = b0 + i;
-          before += __shfl_sync(0xffffffffu, incl - nb, i);
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, incl, 31);
-      }
-      w.unit(a);
-      const int per = w.jhi - w.jlo;
-      w.h = static_cast<int>((beg - before) / per);
-      w.j = w.jlo + static_cast<int>((beg - before) % per);
-      w.left = min(share, total - beg);
-      w.index = beg;
-      w.cut();
-    }
-  }
-  if (!more) return;     // the whole CTA
-
-  // ---- the producer side of this warp: a second walk, NST blocks ahead ----
-  Walk<KB> p = w;
-  bool p_more = true;
-  int pj = 0, seq_p = 0, page_next = -1;
+  // ---- items: the one in hand, and the producer's, NST blocks ahead ----
+  if (!next_item<KB>(a, &items[warp][0], sp, true)) return;     // the whole CTA
+  if (lane == 0) items[warp][1] = items[warp][0];
+  __syncwarp();
+  const Item& w = items[warp][0];
+  Item& p = items[warp][1];
+  // first own block of an item: blocks go to the warps in turn
+  auto first_own = [&](int j) { return j + ((warp - j) & (NW - 1)); };
   bool dead = false;     // a wait ran out: nothing more is copied or computed
-  // first own block of a segment: blocks go to the warps in turn
-  auto first_own = [&](const Walk<KB>& x) { return x.j + static_cast<int>((warp - x.index) & (NW - 1)); };
-  auto settle = [&]() {  // moves p to a segment that has a block for this warp
-    while (p_more && pj >= p.jend) {
-      p_more = p.next(a, unit_step);
-      if (p_more) pj = first_own(p);
+  bool p_more = true;
+  int pj = first_own(p.j), p_end = p.jend, seq_p = 0, page_next = -2;
+  auto settle = [&]() {  // moves p to an item that has a block for this warp
+    while (p_more && pj >= p_end) {
+      p_more = next_item<KB>(a, &p, sp, false);
+      pj = first_own(p.j);
+      p_end = p.jend;
     }
   };
-  auto load_page = [&]() {   // lane i: the page of sub-block i of the next block
+  auto load_page = [&]() {   // lane i: the page of piece i of the next block
     page_next = -2;
     if (p_more && lane < NSUB) {
       const int key = pj * KB + lane * G_::KEYS;
@@ -750,19 +883,19 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
     settle();
     load_page();
   };
-  pj = first_own(p);
   settle();
   load_page();
   for (int s = 0; s < NST; ++s) issue();
 
-  // ---- segments ----
+  // ---- items ----
   int seq_c = 0;
-  while (more) {
+  for (bool more = true; more;) {
     C c;
     c.open(a, w.b, w.h);
     bool any = false;
+    const int lo = w.lo, n = w.n, jend = w.jend;
 
-    for (int j = first_own(w); j < w.jend; j += NW) {
+    for (int j = first_own(w.j); j < jend; j += NW) {
       const int st = seq_c % NST;
       if (!dead && !mbar_wait(&bars[st], (seq_c / NST) & 1)) {
         if (lane == 0) set_error(a.pg.err, DEVERR_TIMEOUT);
@@ -775,7 +908,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
       for (int sub = 0; sub < NSUB; ++sub) {
         if (!((have >> sub) & 1)) continue;
         any = true;
-        c.piece(a, ring + st * G_::STAGE + sub * G_::SUB, sring + st * G_::SCALE + sub * 128, j * KB + sub * G_::KEYS, w.lo, w.n, wbuf, cleared);
+        c.piece(a, ring + st * G_::STAGE + sub * G_::SUB, sring + st * G_::SCALE + sub * 128, j * KB + sub * G_::KEYS, lo, n, wbuf, cleared);
       }
       if (cleared) fence_proxy_async_smem();   // those stores come before the next copy into the stage
       __syncwarp();
@@ -788,9 +921,11 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
     // ---- join the warps ----
     c.close(macc, mml, warp, any);
     __syncthreads();
-    const bool complete = w.j == w.jlo && w.jend == w.jhi;
+    const bool complete = w.parts == 1;
     const int64_t unit = static_cast<int64_t>(w.b) * Hkv + w.h;
-    const int slot = 2 * static_cast<int>(blockIdx.x) + (w.index == share * blockIdx.x ? 0 : 1);
+    // partial i of the sequence: by group, and whether its range begins with this sequence
+    auto slot_of = [&](int i) { return (2 * (w.first + i) + (i == 0 ? w.second : 0)) * Hkv + w.h; };
+    const int slot = complete ? 0 : slot_of(static_cast<int>(blockIdx.x) / Hkv - w.first);
     const int64_t orow = static_cast<int64_t>(w.b) * a.Hq + static_cast<int64_t>(w.h) * G;
     for (int i = threadIdx.x; i < G * (D / 4); i += NW * 32) {
       const int q = i / (D / 4), e = (i % (D / 4)) * 4;
@@ -820,12 +955,9 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
       }
     }
     if (!complete) {
-      // ranges that hold a part of this unit
-      const int64_t ubeg = w.index - (w.j - w.jlo), uend = ubeg + (w.jhi - w.jlo);
-      const int c0 = static_cast<int>(ubeg / share), c1 = static_cast<int>((uend - 1) / share);
       __threadfence();
       __syncthreads();
-      if (threadIdx.x == 0) last_flag = atomicAdd(&sc.ticket[unit], 1) == c1 - c0;
+      if (threadIdx.x == 0) last_flag = atomicAdd(&sc.ticket[unit], 1) == w.parts - 1;
       __syncthreads();
       if (last_flag) {
         __threadfence();
@@ -834,17 +966,33 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
           const int q = i / (D / 4), e = (i % (D / 4)) * 4;
           float M = -INFINITY, L = 0.f, seen = 0.f;
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int c = c0; c <= c1; ++c) {
-            const int64_t sl = static_cast<int64_t>(2 * c + (c == c0 && ubeg != share * c ? 1 : 0)) * G + q;
-            const float4 ml = __ldcg(reinterpret_cast<const float4*>(sc.ml + sl * 4));
-            if (ml.z == 0.f) continue;
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(sc.acc + sl * D + e));
-            const float M1 = fmaxf(M, ml.x), mu = M1 == -INFINITY ? 0.f : M1;
-            const float ca = ex2(M - mu), cb = ex2(ml.x - mu);
-            M = M1; seen += ml.z;
-            L = L * ca + ml.y * cb;
-            o.x = o.x * ca + v.x * cb; o.y = o.y * ca + v.y * cb;
-            o.z = o.z * ca + v.z * cb; o.w = o.w * ca + v.w * cb;
+          constexpr int PB = 8;          // partials on their way at a time
+          for (int c0 = 0; c0 < w.parts; c0 += PB) {
+            float4 ml[PB], v[PB];
+#pragma unroll
+            for (int c = 0; c < PB; ++c) {
+              ml[c] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+              if (c0 + c < w.parts) {
+                const int64_t sl = static_cast<int64_t>(slot_of(c0 + c)) * G + q;
+                ml[c] = __ldcg(reinterpret_cast<const float4*>(sc.ml + sl * 4));
+                v[c] = __ldcg(reinterpret_cast<const float4*>(sc.acc + sl * D + e));
+              }
+            }
+            float M1 = M;
+#pragma unroll
+            for (int c = 0; c < PB; ++c) M1 = fmaxf(M1, ml[c].x);
+            const float mu = M1 == -INFINITY ? 0.f : M1, ca = ex2(M - mu);
+            M = M1;
+            L *= ca; o.x *= ca; o.y *= ca; o.z *= ca; o.w *= ca;
+#pragma unroll
+            for (int c = 0; c < PB; ++c) {
+              if (ml[c].z == 0.f) continue;      // no key in that part
+              const float cb = ex2(ml[c].x - mu);
+              seen += ml[c].z;
+              L = fmaf(cb, ml[c].y, L);
+              o.x = fmaf(cb, v[c].x, o.x); o.y = fmaf(cb, v[c].y, o.y);
+              o.z = fmaf(cb, v[c].z, o.z); o.w = fmaf(cb, v[c].w, o.w);
+            }
           }
           write4(static_cast<T*>(a.out) + (orow + q) * D + e, o, L, seen > 0.f);
           if (a.lse && e == 0) a.lse[orow + q] = seen > 0.f ? ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2 : -INFINITY;
@@ -852,7 +1000,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
       }
     }
     __syncthreads();     // the join's buffers are free again
-    more = w.next(a, unit_step);
+    more = next_item<KB>(a, &items[warp][0], sp, false);
   }
   // copies that a dead warp leaves in flight: wait for them (bounded) before its shared memory goes
   if (dead)
@@ -872,7 +1020,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 template <typename F>
 int with_kernel(int dtype, int d, bool e8, int G, F f) {
 #define KVPOP_ATTEND_F32(DD, PP) \
-  if (d == DD && G <= PP) return f(attend_kernel<FmaPieces<DD, PP>>, FmaPieces<DD, PP>::Geometry::SMEM);
+  if (d == DD && G <= PP) return f(attend_kernel<FmaPieces<DD, PP>>, FmaPieces<DD, PP>::Geometry::SMEM, FmaPieces<DD, PP>::Geometry::CTAS, \
+                                           FmaPieces<DD, PP>::Geometry::KB);
   if (dtype == KVPOP_DTYPE_F32) {
     if (e8) return -2;
     KVPOP_ATTEND_F32(128, 4) KVPOP_ATTEND_F32(128, 8) KVPOP_ATTEND_F32(128, 16)
@@ -881,7 +1030,8 @@ int with_kernel(int dtype, int d, bool e8, int G, F f) {
   }
 #undef KVPOP_ATTEND_F32
 #define KVPOP_ATTEND(DD, EE, PP) \
-  if (d == DD && e8 == EE && G <= PP) return f(attend_kernel<MmaPieces<DD, EE, PP>>, MmaPieces<DD, EE, PP>::Geometry::SMEM);
+  if (d == DD && e8 == EE && G <= PP) return f(attend_kernel<MmaPieces<DD, EE, PP>>, MmaPieces<DD, EE, PP>::Geometry::SMEM, MmaPieces<DD, EE, PP>::Geometry::CTAS, \
+                                                      MmaPieces<DD, EE, PP>::Geometry::KB);
   KVPOP_ATTEND(128, false, 4) KVPOP_ATTEND(128, false, 8) KVPOP_ATTEND(128, false, 16)
   KVPOP_ATTEND(128, true, 4) KVPOP_ATTEND(128, true, 8) KVPOP_ATTEND(128, true, 16)
   KVPOP_ATTEND(64, false, 4) KVPOP_ATTEND(64, false, 8) KVPOP_ATTEND(64, false, 16)
@@ -915,7 +1065,7 @@ int make_attend_map(CUtensorMap* map, void* pages, int dtype, int d, bool e8, in
 }
 
 int prepare_attend(int dtype, int d, bool e8, int G) {
-  return with_kernel(dtype, d, e8, G, [](auto kernel, int smem) {
+  return with_kernel(dtype, d, e8, G, [](auto kernel, int smem, int, int) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess ? 0 : -1;
   });
 }
@@ -927,8 +1077,12 @@ int launch_attend(const CUtensorMap& map, const AttendArgs& a, void* scratch, in
   sc.acc = static_cast<float*>(scratch);
   sc.ml = sc.acc + static_cast<size_t>(kAttendRanges) * 2 * a.G * d;
   sc.ticket = reinterpret_cast<int32_t*>(sc.ml + static_cast<size_t>(kAttendRanges) * 2 * a.G * 4);
-  const int grid = kCtasPerSm * num_sms < kAttendRanges ? kCtasPerSm * num_sms : kAttendRanges;
-  return with_kernel(dtype, d, e8, a.G, [&](auto kernel, int smem) {
+  return with_kernel(dtype, d, e8, a.G, [&](auto kernel, int smem, int ctas, int KB) {
+    // as many CTAs as fit the GPU, and no more than the longest sequences that the tables can name would take
+    int64_t most = ctas * num_sms < kAttendRanges ? ctas * num_sms : kAttendRanges;
+    const int64_t blocks = ((static_cast<int64_t>(a.width) << a.pg.page_shift) + KB - 1) / KB;
+    const int64_t need = a.pg.Hkv * a.batch * ((blocks + kMinShare - 1) / kMinShare);
+    const int grid = static_cast<int>(need < 1 ? 1 : need < most ? need : most);
     kernel<<<grid, NW * 32, smem, st>>>(map, a, sc);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
   });

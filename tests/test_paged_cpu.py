@@ -186,72 +186,102 @@ def test_binding_refuses_host_tensors_and_bad_rope():
 
 # ---- the attention's work split, restated from kvpop_paged_attn.cu ----
 
-NW, MIN_SHARE, UNIT_BLOCKS = 4, 8, 16
+NW, MIN_SHARE, RANGES = 4, 8, 1024
 
 
-def _walk(blocks, hkv, n_cta):
-    """Every CTA's segments: (cta, unit, j, jend, jlo..jhi = 0..blocks, index) and the share (None: whole units)."""
-    total, longest = sum(blocks) * hkv, max(blocks, default=0)
-    if longest <= UNIT_BLOCKS:
-        return [(u % n_cta, u, 0, blocks[u // hkv], 0) for u in range(len(blocks) * hkv) if blocks[u // hkv]], None
-    share = max(-(-total // n_cta), MIN_SHARE)
-    segs = []
-    for c in range(n_cta):
-        beg = share * c
-        if beg >= total:
-            break
-        before = b = 0
-        while before + blocks[b] * hkv <= beg:
-            before += blocks[b] * hkv
-            b += 1
-        h, j = divmod(beg - before, blocks[b])
-        left, index = min(share, total - beg), beg
-        while left > 0:
-            jend = min(blocks[b], j + left)
-            segs.append((c, b * hkv + h, j, jend, index))
-            left -= jend - j
-            index += jend - j
+def _split(blocks, hkv, n_cta):
+    """(share, groups, aligned)"""
+    total, longest, seqs = sum(blocks), max(blocks), sum(n > 0 for n in blocks)
+    groups = max(1, n_cta // hkv)
+    share = min(max(-(-total // groups), MIN_SHARE), 1 << 30)
+    if not 0 < seqs <= groups:
+        return share, groups, False
+
+    def fits(s):
+        return sum(min(-(-n // s), groups + 1) for n in blocks) <= groups
+
+    lo, hi = share, -(-longest // (groups // seqs))
+    if hi <= lo or fits(lo):
+        hi = lo
+    else:
+        while hi - lo > 1 + lo // 32:
+            mid = lo + (hi - lo) // 2
+            lo, hi = (lo, mid) if fits(mid) else (mid, hi)
+    return (hi, groups, True) if hi <= share + share // 5 + 16 else (share, groups, False)
+
+
+def _items(cta, blocks, hkv, n_cta, share, groups, aligned):
+    """A CTA's items: (b, h, j, jend, first, parts, second)."""
+    many = hkv > n_cta
+    grp = 0 if many else cta // hkv
+    out = []
+    for h in range(cta if many else cta - grp * hkv, hkv, n_cta):
+        if grp >= groups:
+            return out
+        target = grp if aligned else grp * share
+        before = 0
+        for b, n in enumerate(blocks):
+            own = -(-n // share) if aligned else n
+            if before + own > target:
+                break
+            before += own
+        else:
+            return out
+        skip = target - before
+        if aligned:
+            out.append((b, h, n * skip // own, n * (skip + 1) // own, grp - skip, own, 0))
+            continue
+        pos, left = target, min(share, sum(blocks) - target)
+        while True:
+            n, beg = blocks[b], pos - skip
+            jend = min(n, skip + left)
+            first = beg // share
+            out.append((b, h, skip, jend, first, (beg + n - 1) // share - first + 1, int(beg != first * share)))
+            left -= jend - skip
+            pos += jend - skip
             if left <= 0:
                 break
-            h += 1
-            if h == hkv:
-                h = 0
+            b, skip = b + 1, 0
+            while blocks[b] == 0:
                 b += 1
-                while not blocks[b]:
-                    b += 1
-            j = 0
-    return segs, share
+    return out
 
 
-@pytest.mark.parametrize("seed", range(60))
+@pytest.mark.parametrize("seed", range(40))
 def test_attention_work_split(seed):
-    """Every block of every unit is covered once; a warp's blocks of a segment
-    partition it; the ranges that the last arriver reads are those that wrote,
-    each from its own slot."""
+    """Every block of every head is covered once; no range is larger than the
+    share; the partials that the last arriver reads are the ones that were
+    written, each in a slot of its own inside the scratch."""
     rng = np.random.default_rng(seed)
-    hkv, n_cta = int(rng.choice([1, 2, 8])), int(rng.choice([4, 296, 512]))
-    blocks = [int(x) for x in rng.integers(0, rng.choice([5, 17, 40, 700]), size=rng.integers(1, 30))]
-    segs, share = _walk(blocks, hkv, n_cta)
-    cover = {u: [] for u in range(len(blocks) * hkv)}
-    slots, parts = set(), {}
-    for c, u, j, jend, index in segs:
-        assert jend > j
-        cover[u].append((j, jend))
-        own = [list(range(j + ((w - index) & (NW - 1)), jend, NW)) for w in range(NW)]
-        assert sorted(sum(own, [])) == list(range(j, jend))
-        if share is not None and (j, jend) != (0, blocks[u // hkv]):
-            ubeg = index - j
-            c0, c1 = ubeg // share, (ubeg + blocks[u // hkv] - 1) // share
-            slot = 2 * c + (0 if index == share * c else 1)
-            assert slot not in slots and c0 <= c <= c1 < n_cta
-            slots.add(slot)
-            assert slot == 2 * c + (1 if c == c0 and ubeg != share * c else 0)      # as the last arriver computes it
-            parts[u] = c1 - c0 + 1
-    for u, n in cover.items():
-        n.sort()
-        at = 0
-        for lo, hi in n:
-            assert lo == at
-            at = hi
-        assert at == blocks[u // hkv]
-        assert parts.get(u, 1) == max(len(n), 1)
+    hkv, n_cta = int(rng.choice([1, 2, 3, 8, 700])), int(rng.choice([4, 296, 592]))
+    blocks = [int(x) for x in rng.integers(0, rng.choice([5, 17, 40, 700]), size=rng.integers(1, 90))]
+    if seed % 3 == 0:
+        blocks[0] *= 50
+    if seed % 4 == 0:
+        blocks = [max(blocks[0], 1)] * len(blocks)
+    share, groups, aligned = _split(blocks, hkv, n_cta)
+    cover, written, read, used = {}, {}, {}, set()
+    for cta in range(n_cta):
+        items = _items(cta, blocks, hkv, n_cta, share, groups, aligned)
+        assert sum(x[3] - x[2] for x in items) <= share * -(-hkv // n_cta)
+        for b, h, j, jend, first, parts, second in items:
+            assert j < jend
+            cover.setdefault((b, h), []).append((j, jend, parts))
+            own = [list(range(j + ((w - j) & (NW - 1)), jend, NW)) for w in range(NW)]
+            assert sorted(sum(own, [])) == list(range(j, jend))
+            if parts > 1:
+                def slot_of(i):
+                    return (2 * (first + i) + (second if i == 0 else 0)) * hkv + h
+                mine = slot_of(cta // hkv - first)
+                assert mine not in used and mine < 2 * n_cta <= 2 * RANGES
+                used.add(mine)
+                written.setdefault((b, h), set()).add(mine)
+                if (b, h) not in read:
+                    read[b, h] = {slot_of(i) for i in range(parts)}
+    for b, n in enumerate(blocks):
+        for h in range(hkv):
+            got = sorted(cover.get((b, h), []))
+            assert [x[0] for x in got] == ([0] + [x[1] for x in got[:-1]])[:len(got)]
+            assert (got[-1][1] if got else 0) == n
+            assert all(x[2] == len(got) for x in got)
+    assert read == written
