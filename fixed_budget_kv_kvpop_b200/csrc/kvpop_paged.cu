@@ -4,6 +4,7 @@
 // All are one pass over rows of d elements.
 #include "kvpop_paged.cuh"
 
+#include <atomic>
 #include <cuda_fp8.h>
 #include <type_traits>
 
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  wait_for_prior_kernel();
   // positions and slots are read one token ahead, frequencies before the first copies are asked for
   int pos_next = 0, slot_next = -1;
   auto look = [&](int t) {
@@ -412,6 +414,7 @@ constexpr int heads_smem() { return (kThreads / 32) * ((sizeof(T) == 2 ? 6 : 4) 
 template <typename T, int D, bool E4M3>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ HeadsArgs a, int passes, int chunk) {
   constexpr int LPR = E4M3 ? D / 16 : D / 8, RPW = 32 / LPR, U = E4M3 ? 2 : 4;
+  wait_for_prior_kernel();
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
   const int t = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
   if (t >= a.batch * a.n_tokens) return;
@@ -483,6 +486,7 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   constexpr int PER = 16 / (E4M3 ? 1 : static_cast<int>(sizeof(T)));    // elements per lane
   constexpr int LPR = D / PER, STEP = kThreads / LPR, U = (kGatherTokens + STEP - 1) / STEP;
   const int l = threadIdx.x % LPR;
+  wait_for_prior_kernel();
   const int b = blockIdx.z, h = blockIdx.y >> 1, kv = blockIdx.y & 1;
   int n = a.lens[b];
   const int64_t cap = min(static_cast<int64_t>(a.n_tokens), static_cast<int64_t>(a.width) << a.pg.page_shift);
@@ -540,8 +544,7 @@ int append_t(const HeadsArgs& a, int num_sms, cudaStream_t st) {
   // few tokens: one pass per warp, the shortest way through
   const int chunk = static_cast<int64_t>(tokens) * passes < 16 * num_sms ? 1 : passes;
   const dim3 grid((tokens + W - 1) / W, 2 * ((passes + chunk - 1) / chunk));
-  append_kernel<T, D, E4M3><<<grid, kThreads, 0, st>>>(a, passes, chunk);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return launch_dependent(append_kernel<T, D, E4M3>, grid, kThreads, 0, st, a, passes, chunk);
 }
 
 template <typename T, int D, bool E4M3, int MODE>
@@ -560,9 +563,19 @@ int new_heads_t(const HeadsArgs& a, int num_sms, cudaStream_t st) {
                       : a.rope.rot % 16 == 0 ? heads_kernel<T, D, E4M3, MODE, false, true>
                                              : heads_kernel<T, D, E4M3, MODE, false, false>;
   constexpr int smem = heads_smem<T, D>();
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
-  kernel<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a, q_passes, kv_passes, shift);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  if (smem > 48 * 1024) {
+    // once for each device (up to 64 of them) and variant
+    static std::atomic<uint64_t> done[3];
+    const int which = a.rope.interleaved ? 0 : a.rope.rot % 16 == 0 ? 1 : 2;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return -1;
+    const uint64_t bit = UINT64_C(1) << (device & 63);
+    if (device > 63 || !(done[which].load(std::memory_order_relaxed) & bit)) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
+      done[which].fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(grid)), kThreads, smem, st, a, q_passes, kv_passes, shift);
 }
 
 template <typename T, int D, bool E4M3>
@@ -575,8 +588,7 @@ int heads_t(const HeadsArgs& a, int mode, int num_sms, cudaStream_t st) {
 template <typename T, int D, bool E4M3>
 int gather_t(const GatherArgs& a, cudaStream_t st) {
   const dim3 grid((a.n_tokens + kGatherTokens - 1) / kGatherTokens, a.pg.Hkv * 2, a.batch);
-  gather_kernel<T, D, E4M3><<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return launch_dependent(gather_kernel<T, D, E4M3>, grid, kThreads, 0, st, a);
 }
 
 }  // namespace

@@ -73,6 +73,29 @@ struct AttendArgs {
   int window;
 };
 
+// Programmatic dependent launch: a kernel's blocks may be set up while the
+// kernel before it in the stream still runs.  Every kernel launched so waits
+// here before its first access to global memory (until that kernel has ended
+// and its writes are visible), and lets the next one be set up.
+__device__ __forceinline__ void wait_for_prior_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+int launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess ? 0 : -1;
+}
+
 enum HeadsMode : int { HEADS_DENSE = 0, HEADS_APPEND = 1, HEADS_STEP = 2 };
 
 // All return 0, -1 (a CUDA call failed) or -2 (shape not built).

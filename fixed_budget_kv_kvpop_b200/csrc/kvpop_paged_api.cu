@@ -1,5 +1,6 @@
 // Host side of the paged cache and of kvpop_qk_norm_rope (include/kvpop.h):
 // validation, device buffer layout, launches.
+#include <atomic>
 #include <cmath>
 #include <new>
 
@@ -113,8 +114,12 @@ bool rope_args(const kvpop_rope* r, int head_dim, RopeArgs* out, int* status) {
 }
 
 int sm_count(int device) {
-  int sms = 0;
-  return cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) == cudaSuccess ? sms : 0;
+  static std::atomic<int> known[64];     // a device's count does not change
+  int sms = device < 64 ? known[device].load(std::memory_order_relaxed) : 0;
+  if (sms != 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 0;
+  if (device < 64) known[device].store(sms, std::memory_order_relaxed);
+  return sms;
 }
 
 int status_of(int r) { return r == 0 ? KVPOP_OK : r == -2 ? KVPOP_ERR_BAD_SHAPE : KVPOP_ERR_CUDA; }

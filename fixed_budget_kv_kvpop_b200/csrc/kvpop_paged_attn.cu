@@ -756,6 +756,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   }
   __syncwarp();
 
+  wait_for_prior_kernel();
   // ---- the split ----
   const int Hkv = a.pg.Hkv, G = a.G, n_cta = gridDim.x;
   Split sp;
@@ -1083,8 +1084,7 @@ int launch_attend(const CUtensorMap& map, const AttendArgs& a, void* scratch, in
     const int64_t blocks = ((static_cast<int64_t>(a.width) << a.pg.page_shift) + KB - 1) / KB;
     const int64_t need = a.pg.Hkv * a.batch * ((blocks + kMinShare - 1) / kMinShare);
     const int grid = static_cast<int>(need < 1 ? 1 : need < most ? need : most);
-    kernel<<<grid, NW * 32, smem, st>>>(map, a, sc);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    return launch_dependent(kernel, dim3(grid), NW * 32, smem, st, map, a, sc);
   });
 }
 
