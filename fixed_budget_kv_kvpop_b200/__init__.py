@@ -1,7 +1,8 @@
 """Python binding of libkvpop.so (the KVpop fixed-budget KV cache C ABI).
 
 Argument marshalling only: every step of the decode path runs in the CUDA
-kernels behind include/kvpop.h.  PyTorch supplies device memory and streams.
+kernels behind include/kvpop.h.  The paged calls are marshalled by _binding
+(csrc/binding.cpp), the others by ctypes.  PyTorch supplies device memory and streams.
 Importing this module loads the in-tree libkvpop.so and fails loudly if it is
 missing; there is no fallback implementation.
 
@@ -111,10 +112,7 @@ class kvpop_paged_layout_info(ctypes.Structure):
         "pages_offset", "pages_layer_stride", "scales_offset", "scales_layer_stride")]
 
 
-# kvpop_rows, kvpop_rope and kvpop_attend_options, packed for one call each
-_pack_rows = struct.Struct("@Pqqq").pack
-_pack_rope = struct.Struct("@PPPffii").pack
-_pack_attend_options = struct.Struct("@ffi").pack
+_pack_rope = struct.Struct("@PPPffii").pack    # kvpop_rope
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -164,6 +162,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 
 lib = load_library()
+
+try:
+    from . import _binding
+except ImportError as e:
+    raise ImportError(f"{_HERE}/_binding.so does not load ({e}): run `python fixed_budget_kv_kvpop_b200/csrc/build.py`") from e
+
+
+def _addresses(library) -> dict:
+    """Addresses of the calls that _binding makes, in one build of the library."""
+    return {name: ctypes.cast(getattr(library, name), ctypes.c_void_p).value for name in (
+        "kvpop_qk_norm_rope", "kvpop_paged_append", "kvpop_paged_append_qkv", "kvpop_paged_gather",
+        "kvpop_paged_attend")}
+
+
+_FN = _addresses(lib)
 
 
 class KVPopError(RuntimeError):
@@ -458,59 +471,6 @@ class KVPopCache:
 
 # ---- heads of new tokens, and the paged (full) cache ----
 
-# These calls are made once per layer and token, and the kernels behind the
-# small ones run for 3 to 6 us: the checks below read each attribute once.
-
-def _stream_on(device, stream) -> Optional[int]:
-    """The given stream, or `device`'s current one (which need not be the current device's)."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _rows(t, name: str, shape, dtype, device, written: bool = False) -> bytes:
-    """A kvpop_rows of `t`, rows [batch][token][head][head_dim] with the last
-    dimension contiguous: any strides of whole 16 bytes.  Raises ValueError on
-    anything else; the C ABI sees only addresses."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name}: on {t.device}, expected the cuda device {device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    sb, st, sh, sd = t.stride()
-    at = t.data_ptr()
-    unit = 4 if dtype is torch.float32 else 8
-    if sd != 1 or at & 15 or (sb | st | sh) % unit or (written and not (sb and st and sh)):
-        # something is odd; strides of dimensions of one row or none do not count
-        b, n, h, _ = shape
-        used = [s for s, m in ((sb, b), (st, n), (sh, h)) if m > 1]
-        if b and n:
-            if sd != 1 or at & 15 or any(s % unit for s in used):
-                raise ValueError(f"{name}: strides {t.stride()} at {at:#x}: rows must be contiguous and start on "
-                                 "16 bytes")
-            if written and not all(used):
-                raise ValueError(f"{name}: an expanded tensor cannot be written")
-    return _pack_rows(at, sb, st, sh)
-
-
-def _dense(t, name: str, shape, dtype, device) -> None:
-    """check_tensor, with its message for anything that is not as it should be."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
-            and t.is_contiguous()):
-        check_tensor(t, name, shape, dtype, device)
-
-
-def _ints(t, name: str, shape, device) -> int:
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.shape != shape or t.device != device \
-            or not t.is_contiguous():
-        what = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__
-        raise ValueError(f"{name}: expected a contiguous int32 tensor {tuple(shape)} on {device}, got {what}")
-    return t.data_ptr()
-
-
 class Rope:
     """Norm weights and rotation of query and key heads (kvpop_rope); keeps
     its tensors alive.  Made by make_rope."""
@@ -520,8 +480,9 @@ class Rope:
         self.device = inv_freq.device
         self.rot_dim = 2 * inv_freq.numel()
         self.head_dim = next((w.numel() for w in (q_weight, k_weight) if w is not None), None)
-        self.packed = _pack_rope(_ptr(q_weight) or 0, _ptr(k_weight) or 0, inv_freq.data_ptr(), eps, scale,
-                                 self.rot_dim, int(bool(interleaved)))
+        packed = _pack_rope(_ptr(q_weight) or 0, _ptr(k_weight) or 0, inv_freq.data_ptr(), eps, scale,
+                            self.rot_dim, int(bool(interleaved)))
+        self._args = (packed, self.device.index, self.head_dim or 0)
 
 
 def make_rope(inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6, scale: float = 1.0,
@@ -548,13 +509,10 @@ def make_rope(inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6, scal
     return Rope(inv_freq, q_weight, k_weight, eps, scale, interleaved)
 
 
-def _check_rope(rope, head_dim, device):
+def _rope_args(rope):
     if not isinstance(rope, Rope):
         raise ValueError(f"rope: expected a Rope (make_rope), got {type(rope).__name__}")
-    if rope.device != device:
-        raise ValueError(f"rope: on {rope.device}, the rows are on {device}")
-    if rope.head_dim not in (None, head_dim):
-        raise ValueError(f"rope: weights of {rope.head_dim} elements, head_dim is {head_dim}")
+    return rope._args
 
 
 def qk_norm_rope(rope: Rope, q, k, positions, q_out, k_out, stream=None) -> None:
@@ -563,20 +521,7 @@ def qk_norm_rope(rope: Rope, q, k, positions, q_out, k_out, stream=None) -> None
     heads; any strides of whole 16 bytes (views of a projection's output,
     transposed views of head-major buffers), q_out = q and k_out = k among
     them.  positions: int32 [batch][tokens]."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 4 or q.device.type != "cuda":
-        raise ValueError("q: expected a cuda tensor [batch][tokens][heads][head_dim]")
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise ValueError("k: expected a cuda tensor [batch][tokens][heads][head_dim]")
-    dtype, device, qs = q.dtype, q.device, q.shape
-    b, n, hq, d = qs
-    hkv = k.shape[2]
-    ks = (b, n, hkv, d)
-    _check_rope(rope, d, device)
-    _check(lib.kvpop_qk_norm_rope(dtype_code(dtype), d, hq, hkv, rope.packed, b, n,
-                                  _rows(q, "q", qs, dtype, device), _rows(k, "k", ks, dtype, device),
-                                  _ints(positions, "positions", (b, n), device),
-                                  _rows(q_out, "q_out", qs, dtype, device, True),
-                                  _rows(k_out, "k_out", ks, dtype, device, True), _stream_on(device, stream)),
+    _check(_binding.qk_norm_rope(_FN["kvpop_qk_norm_rope"], _rope_args(rope), q, k, positions, q_out, k_out, stream),
            "kvpop_qk_norm_rope")
 
 
@@ -610,7 +555,6 @@ class KVPopPagedCache:
         self.nbytes = paged_bytes(cfg, self._lib)
         self.buffer = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device or "cuda")
         self.device = self.buffer.device
-        self._kv = (cfg.n_kv_heads, cfg.head_dim)
         base = self.buffer.data_ptr()
         self._off = (-base) % 256
         self.handle = ctypes.c_void_p()
@@ -618,6 +562,10 @@ class KVPopPagedCache:
             _check(self._lib.kvpop_paged_create(ctypes.byref(cfg), ctypes.c_void_p(base + self._off), self.nbytes,
                                                 ctypes.byref(self.handle)), "kvpop_paged_create")
         self.dtype = _torch_dtype(cfg.dtype)
+        fn = _FN if self._lib is lib else _addresses(self._lib)
+        self._append, self._append_qkv, self._gather, self._attend = (
+            fn["kvpop_paged_" + name] for name in ("append", "append_qkv", "gather", "attend"))
+        self._args = (self.handle.value, cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim, cfg.dtype, self.device.index)
         lay, e8 = self.layout(), cfg.cache_format == KVPOP_CACHE_E4M3
         shape = (cfg.n_pages, cfg.n_kv_heads, 2, cfg.page_size, cfg.head_dim)
         held = torch.float8_e4m3fn if e8 else self.dtype
@@ -631,56 +579,24 @@ class KVPopPagedCache:
             self._lib.kvpop_paged_destroy(h)
             self.handle = None
 
-    def _kv_shape(self, t, name):
-        if not isinstance(t, torch.Tensor) or t.dim() != 4:
-            raise ValueError(f"{name}: expected a cuda tensor [batch][tokens][heads][head_dim]")
-        return t.shape[:2] + self._kv
-
     def append(self, layer: int, k, v, slots, stream=None) -> None:
         """Writes keys and values, [batch][tokens][KV heads][head_dim], to the
         rows that slots (int32 [batch][tokens]: page * page_size + row;
         negative: written nowhere) name.  No two tokens may share a slot."""
-        shape = self._kv_shape(k, "k")
-        b, n = shape[0], shape[1]
-        _check(self._lib.kvpop_paged_append(self.handle, layer, _rows(k, "k", shape, self.dtype, self.device),
-                                            _rows(v, "v", shape, self.dtype, self.device),
-                                            _ints(slots, "slots", (b, n), self.device), b, n,
-                                            _stream_on(self.device, stream)), "kvpop_paged_append")
+        _check(_binding.append(self._append, self._args, layer, k, v, slots, stream), "kvpop_paged_append")
 
     def append_qkv(self, layer: int, rope: Rope, q, k, v, positions, slots, q_out, stream=None) -> None:
         """qk_norm_rope and append in one launch: normalised and turned queries
         go to q_out, keys and values to their slots."""
-        shape = self._kv_shape(k, "k")
-        b, n, d = shape[0], shape[1], shape[3]
-        qs = (b, n, self.cfg.n_q_heads, d)
-        _check_rope(rope, d, self.device)
-        _check(self._lib.kvpop_paged_append_qkv(self.handle, layer, rope.packed,
-                                                _rows(q, "q", qs, self.dtype, self.device),
-                                                _rows(k, "k", shape, self.dtype, self.device),
-                                                _rows(v, "v", shape, self.dtype, self.device),
-                                                _ints(positions, "positions", (b, n), self.device),
-                                                _ints(slots, "slots", (b, n), self.device),
-                                                _rows(q_out, "q_out", qs, self.dtype, self.device, True), b, n,
-                                                _stream_on(self.device, stream)), "kvpop_paged_append_qkv")
-
-    def _table(self, page_table, lens, b):
-        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
-            raise ValueError("page_table: expected an int32 cuda tensor [batch][pages]")
-        width = page_table.shape[1]
-        return (_ints(page_table, "page_table", (b, width), self.device), width,
-                _ints(lens, "lens", (b,), self.device))
+        _check(_binding.append_qkv(self._append_qkv, self._args, layer, _rope_args(rope), q, k, v, positions, slots,
+                                   q_out, stream), "kvpop_paged_append_qkv")
 
     def gather(self, layer: int, page_table, lens, k_out, v_out, stream=None) -> None:
         """Reads sequences back: the first lens[b] tokens of sequence b, whose
         pages are page_table[b] (int32 [batch][pages]), go to k_out and v_out,
         [batch][tokens][KV heads][head_dim]; rows behind them stay as they were."""
-        shape = self._kv_shape(k_out, "k_out")
-        b, n = shape[0], shape[1]
-        table, width, lens_p = self._table(page_table, lens, b)
-        _check(self._lib.kvpop_paged_gather(self.handle, layer, table, width, width, lens_p, b, n,
-                                            _rows(k_out, "k_out", shape, self.dtype, self.device, True),
-                                            _rows(v_out, "v_out", shape, self.dtype, self.device, True),
-                                            _stream_on(self.device, stream)), "kvpop_paged_gather")
+        _check(_binding.gather(self._gather, self._args, layer, page_table, lens, k_out, v_out, stream),
+               "kvpop_paged_gather")
 
     def attend(self, layer: int, q, page_table, lens, out, lse=None, scale=0.0, softcap=0.0, window=0,
                stream=None) -> None:
@@ -688,19 +604,8 @@ class KVPopPagedCache:
         [head_dim]; lse fp32 [batch][q heads] or None.  scale 0: 1 / sqrt(head_dim);
         softcap > 0: scores become softcap * tanh(score / softcap); window > 0:
         the last `window` tokens alone are attended."""
-        c = self.cfg
-        if not isinstance(q, torch.Tensor) or q.dim() != 3:
-            raise ValueError("q: expected a cuda tensor [batch][q heads][head_dim]")
-        b = q.shape[0]
-        shape, device = (b, c.n_q_heads, c.head_dim), self.device
-        _dense(q, "q", shape, self.dtype, device)
-        _dense(out, "out", shape, self.dtype, device)
-        if lse is not None:
-            _dense(lse, "lse", shape[:2], torch.float32, device)
-        table, width, lens_p = self._table(page_table, lens, b)
-        _check(self._lib.kvpop_paged_attend(self.handle, layer, q.data_ptr(), table, width, width, lens_p, b,
-                                            _pack_attend_options(scale, softcap, window), out.data_ptr(), _ptr(lse),
-                                            _stream_on(self.device, stream)), "kvpop_paged_attend")
+        _check(_binding.attend(self._attend, self._args, layer, q, page_table, lens, out, lse, scale, softcap, window,
+                               stream), "kvpop_paged_attend")
 
     def _view(self, offset, shape, dtype):
         n = dtype.itemsize
@@ -733,5 +638,6 @@ class KVPopPagedCache:
         return st, bits.value
 
     def clear_error(self, stream=None):
-        _check(self._lib.kvpop_paged_clear_error(self.handle, _stream_on(self.device, stream)),
-               "kvpop_paged_clear_error")
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        _check(self._lib.kvpop_paged_clear_error(self.handle, stream.cuda_stream), "kvpop_paged_clear_error")

@@ -67,6 +67,33 @@ def build(force: bool = False, verbose: bool = False, out: str = OUT, defines=()
     return out
 
 
+BINDING_SOURCE = os.path.join(HERE, "binding.cpp")
+BINDING_OUT = os.path.join(PKG, "_binding.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """Compiles the Python side of the paged calls (host code only) against
+    the torch and Python that run this."""
+    deps = [BINDING_SOURCE, os.path.join(ROOT, "include", "kvpop.h"), __file__]
+    if not force and os.path.exists(BINDING_OUT) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING_OUT) for p in deps):
+        return BINDING_OUT
+    import sysconfig
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I" + os.path.join(home, "include"), "-I" + os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), BINDING_SOURCE,
+           "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-o", BINDING_OUT + ".tmp"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("g++ failed building _binding.so")
+    os.replace(BINDING_OUT + ".tmp", BINDING_OUT)
+    return BINDING_OUT
+
+
 TEST_HOOKS_OUT = os.path.join(PKG, "libkvpop_testhooks.so")
 # The failure-injection build: kvpop_debug_set_hook works, and the decode
 # kernel's merge-queue waits give up after 50 ms instead of 2 s.
@@ -85,5 +112,6 @@ def build_test_hooks(force: bool = False) -> str:
 
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(build_binding(force="--force" in sys.argv))
     if "--test-hooks" in sys.argv:
         print(build_test_hooks(force="--force" in sys.argv))

@@ -86,12 +86,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Attended tokens [lo, n) of sequence b.  Lengths outside the table are cut.
+// Attended tokens [lo, n) of a sequence whose length is given as n; lengths outside the table are cut.
 struct Span {
   int lo, n;
 };
-__device__ __forceinline__ Span span_of(const AttendArgs& a, int b) {
-  int n = a.lens[b];
+__device__ __forceinline__ Span span_of(const AttendArgs& a, int n) {
   const int64_t cap = static_cast<int64_t>(a.width) << a.pg.page_shift;
   n = n < 0 ? 0 : n > cap ? static_cast<int>(cap) : n;
   return Span{a.window > 0 && n > a.window ? n - a.window : 0, n};
@@ -100,7 +99,7 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int b) {
 // Blocks of sequence b.
 template <int KB>
 __device__ __forceinline__ int blocks_of(const AttendArgs& a, int b) {
-  const Span s = span_of(a, b);
+  const Span s = span_of(a, a.lens[b]);
   return (s.n + KB - 1) / KB - s.lo / KB;
 }
 
@@ -158,18 +157,20 @@ __device__ __noinline__ bool next_item(const AttendArgs& a, Item* it, const Spli
       int nb = 0;
       if (b0 + lane < a.batch) nb = b0 == 0 ? sp.nb0 : blocks_of<KB>(a, b0 + lane);
       const int own = sp.aligned ? (nb + sp.share - 1) / sp.share : nb;
-      int64_t sum = own;
+      uint32_t sum = own;            // 32 sequences of at most 2^26 blocks
+      if (a.batch > 1) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += u;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += u;
+        }
       }
       const unsigned past = __ballot_sync(0xffffffffu, before + sum > target);
       if (past) {
         const int i = __ffs(past) - 1;
         b = b0 + i;
         parts = __shfl_sync(0xffffffffu, own, i);
-        skip = static_cast<int>(target - before - (__shfl_sync(0xffffffffu, sum, i) - parts));
+        skip = static_cast<int>(target - before - (__shfl_sync(0xffffffffu, sum, i) - static_cast<uint32_t>(parts)));
         break;
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
@@ -180,7 +181,7 @@ __device__ __noinline__ bool next_item(const AttendArgs& a, Item* it, const Spli
   }
   __syncwarp();                      // the old item has been read
   if (lane == 0) {
-    const Span s = span_of(a, b);
+    const Span s = span_of(a, a.lens[b]);
     const int j0 = s.lo / KB, nb = (s.n + KB - 1) / KB - j0;
     Item x;
     x.b = b; x.h = h; x.lo = s.lo; x.n = s.n; x.pos = pos;
@@ -768,18 +769,15 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
       const int b = b0 + lane;
       int nb = 0;
       if (b < a.batch) {
-        nb = blocks_of<KB>(a, b);
-        bad_len |= a.lens[b] != span_of(a, b).n;
+        const int given = a.lens[b];
+        const Span s = span_of(a, given);
+        nb = (s.n + KB - 1) / KB - s.lo / KB;
+        bad_len |= given != s.n;
       }
       if (b0 == 0) sp.nb0 = nb;
-      total += nb;
-      longest = max(longest, nb);
+      total += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(nb));     // 32 sequences of at most 2^26 blocks
+      longest = max(longest, __reduce_max_sync(0xffffffffu, nb));
       seqs += __popc(__ballot_sync(0xffffffffu, nb > 0));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      total += __shfl_xor_sync(0xffffffffu, total, o);
-      longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
     }
     if (bad_len && blockIdx.x == 0 && warp == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
     sp.total = total;
@@ -818,7 +816,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
 
   // sequences without a token
   for (int b = blockIdx.x; b < a.batch; b += n_cta) {
-    if (span_of(a, b).n > 0) continue;
+    if (span_of(a, a.lens[b]).n > 0) continue;
     for (int i = threadIdx.x; i < a.Hq * D; i += NW * 32)
       static_cast<T*>(a.out)[static_cast<int64_t>(b) * a.Hq * D + i] = Elem<T>::from_f32(0.f);
     if (a.lse)

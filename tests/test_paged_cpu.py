@@ -1,5 +1,6 @@
 """Paged cache and heads: the oracle's own checks, and every refusal that needs no GPU."""
 import ctypes
+import struct
 
 import numpy as np
 import pytest
@@ -8,6 +9,7 @@ import torch
 import fixed_budget_kv_kvpop_b200 as kp
 from oracle import paged_oracle as po
 
+ROWS = struct.Struct("@Pqqq")     # kvpop_rows
 CFG = dict(n_layers=2, n_q_heads=8, n_kv_heads=2, head_dim=128, page_size=16, n_pages=10, max_batch=4)
 
 
@@ -140,7 +142,7 @@ def _heads_call(dtype=kp.KVPOP_DTYPE_BF16, d=128, hq=4, hkv=2, rope=None, batch=
     """kvpop_qk_norm_rope on host memory: every argument but that is in order."""
     buf = ctypes.create_string_buffer(8192)
     base = (ctypes.addressof(buf) + 255) // 256 * 256
-    r = kp._pack_rows(base if addr is None else addr, *strides)
+    r = ROWS.pack(base if addr is None else addr, *strides)
     rope = kp._pack_rope(0, 0, base, 1e-6, 1.0, 128, 0) if rope is None else rope
     return kp.lib.kvpop_qk_norm_rope(dtype, d, hq, hkv, rope, batch, n, r, r, base + pos if pos else None, r, r, None)
 
@@ -168,20 +170,31 @@ def test_heads_refusals(kw, code):
     assert _heads_call(**kw) == code
 
 
-def test_binding_refuses_host_tensors_and_bad_rope():
+def test_binding_refuses_what_is_not_a_cuda_tensor():
     f = torch.zeros(32, dtype=torch.float64)
     with pytest.raises(ValueError, match="cuda"):
         kp.make_rope(f)
-    q = torch.zeros(1, 1, 4, 64)
+    q, pos = torch.zeros(1, 1, 4, 64), torch.zeros(1, 1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="Rope"):
+        kp.qk_norm_rope(None, q, q, pos, q, q)
+    rope = (bytes(40), 0, 64)
     with pytest.raises(ValueError, match="cuda"):
-        kp.qk_norm_rope(None, q, q, torch.zeros(1, 1, dtype=torch.int32), q, q)
-    dev = torch.device("cuda", 0)
-    with pytest.raises(ValueError, match="expected the cuda device"):
-        kp._rows(q, "q", q.shape, torch.float32, dev)
+        kp._binding.qk_norm_rope(kp._FN["kvpop_qk_norm_rope"], rope, q, q, pos, q, q, None)
     with pytest.raises(ValueError, match="torch.Tensor"):
-        kp._rows([1.0], "q", (1,), torch.float32, dev)
-    with pytest.raises(ValueError, match="int32"):
-        kp._ints(torch.zeros(3, dtype=torch.int64), "slots", (3,), dev)
+        kp._binding.qk_norm_rope(kp._FN["kvpop_qk_norm_rope"], rope, [1.0], q, pos, q, q, None)
+    with pytest.raises(ValueError, match="batch"):
+        kp._binding.qk_norm_rope(kp._FN["kvpop_qk_norm_rope"], rope, q[0], q, pos, q, q, None)
+    with pytest.raises(TypeError):
+        kp._binding.qk_norm_rope(kp._FN["kvpop_qk_norm_rope"], rope)
+    cache = (0, 4, 4, 64, kp.KVPOP_DTYPE_F32, 0)
+    with pytest.raises(ValueError, match="k: on cpu, expected the cuda device 0"):
+        kp._binding.append(kp._FN["kvpop_paged_append"], cache, 0, q, q, pos, None)
+    with pytest.raises(ValueError, match="q: on cpu"):
+        kp._binding.attend(kp._FN["kvpop_paged_attend"], cache, 0, q[0], pos, pos, q[0], None, 0.0, 0.0, 0, None)
+    with pytest.raises(ValueError, match="32 bits"):
+        kp._binding.append(kp._FN["kvpop_paged_append"], cache, 1 << 40, q, q, pos, None)
+    with pytest.raises(ValueError, match="six"):
+        kp._binding.append(kp._FN["kvpop_paged_append"], (0, 4), 0, q, q, pos, None)
 
 
 # ---- the attention's work split, restated from kvpop_paged_attn.cu ----
