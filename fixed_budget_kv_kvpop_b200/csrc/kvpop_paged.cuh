@@ -71,6 +71,7 @@ struct AttendArgs {
   int batch, width, Hq, G;
   float scale, softcap;
   int window;
+  int fixed;        // > 0: parts of kMinShare blocks, this many groups of CTAs for each sequence (set by launch_attend)
 };
 
 // Programmatic dependent launch: a kernel's blocks may be set up while the

@@ -9,7 +9,10 @@
 // they lie).  The groups either take one part of one sequence each, all parts
 // as even as they come, or, where that leaves the largest part well above the
 // average, equal contiguous ranges of all sequences' blocks.  Every CTA finds
-// its range from the lengths on the device.  Where a sequence lies in several
+// its range from the lengths on the device.  Where the page table is so narrow
+// that even the longest sequences it can hold give no more parts of kMinShare
+// blocks than there are groups, those are the parts, and nothing is searched
+// for: short calls are a chain of latencies, of which the search was a third.  Where a sequence lies in several
 // ranges, each leaves a partial (accumulator, running maximum, sum), and the
 // CTA that arrives last joins them in their order, so results do not depend on
 // who is last.
@@ -131,6 +134,22 @@ struct Item {
   int64_t pos;       // of the item's first block among all blocks (ranges)
 };
 
+// The item of a group where parts are fixed: kMinShare blocks of one sequence.
+template <int KB>
+__device__ __forceinline__ bool fixed_item(const AttendArgs& a, Item* it, int grp, int h) {
+  const int b = grp / a.fixed, part = grp - b * a.fixed;
+  const Span s = span_of(a, a.lens[b]);
+  const int j0 = s.lo / KB, nb = (s.n + KB - 1) / KB - j0;
+  if (part * kMinShare >= nb) return false;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    const int j = j0 + part * kMinShare, jend = min(j + kMinShare, j0 + nb);
+    *it = Item{b, h, s.lo, s.n, j, jend, grp - part, (nb + kMinShare - 1) / kMinShare, 0, jend - j, 0};
+  }
+  __syncwarp();
+  return true;
+}
+
 // The CTA's first or next item (the whole warp together); false at the end.
 // CTAs take one head, or with more heads than CTAs every gridDim.x-th.
 template <int KB>
@@ -149,6 +168,7 @@ __device__ __noinline__ bool next_item(const AttendArgs& a, Item* it, const Spli
   } else {
     h = start ? (many ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) - grp * Hkv) : it->h + n_cta;
     if (h >= Hkv || grp >= sp.groups) return false;
+    if (a.fixed > 0) return fixed_item<KB>(a, it, grp, h);
     // the sequence in which the range begins
     const int64_t target = sp.aligned ? grp : static_cast<int64_t>(grp) * sp.share;
     int64_t before = 0;
@@ -221,7 +241,7 @@ struct Geo {
   static constexpr int SCALE = E4M3 ? NSUB * 128 : 0;        // bytes of scales of a stage
   static constexpr int MERGE = NW * GP * (D + 4) * 4;
   static constexpr int WEIGHTS = F32 ? NW * KEYS * 16 : 0;   // fp32: weights of a piece for four heads
-  static constexpr int CTAS = GP == 16 ? 2 : GP == 8 ? KV_C8 : F32 ? KV_CF : E4M3 ? KV_CE : KV_C4;    // per SM
+  static constexpr int CTAS = GP == 16 ? 2 : GP == 8 ? KV_C8 : F32 ? (D == 64 ? 3 : 2) : E4M3 ? KV_CE : KV_C4;    // per SM
   static constexpr int CTA = (228 * 1024) / CTAS - 1024;
   static constexpr int NST0 = (CTA - 1024 - MERGE - WEIGHTS - 512) / (NW * (STAGE + SCALE + 16));
   static constexpr int NST = NST0 > 8 ? 8 : NST0;
@@ -761,7 +781,12 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   // ---- the split ----
   const int Hkv = a.pg.Hkv, G = a.G, n_cta = gridDim.x;
   Split sp;
-  {
+  sp.groups = max(1, n_cta / Hkv);
+  if (a.fixed > 0) {
+    sp.aligned = true;
+    if (warp == 0 && lane == 0 && blockIdx.x < a.batch && a.lens[blockIdx.x] != span_of(a, a.lens[blockIdx.x]).n)
+      set_error(a.pg.err, DEVERR_BAD_INDEX);
+  } else {
     int64_t total = 0;
     int longest = 0, seqs = 0;
     bool bad_len = false;
@@ -781,7 +806,6 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
     }
     if (bad_len && blockIdx.x == 0 && warp == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
     sp.total = total;
-    sp.groups = max(1, n_cta / Hkv);
     const int64_t even = quotient(total + sp.groups - 1, sp.groups);
     sp.share = static_cast<int>(min(max(even, static_cast<int64_t>(kMinShare)), static_cast<int64_t>(1 << 30)));
     sp.aligned = false;
@@ -815,16 +839,23 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   }
 
   // sequences without a token
-  for (int b = blockIdx.x; b < a.batch; b += n_cta) {
-    if (span_of(a, a.lens[b]).n > 0) continue;
-    for (int i = threadIdx.x; i < a.Hq * D; i += NW * 32)
-      static_cast<T*>(a.out)[static_cast<int64_t>(b) * a.Hq * D + i] = Elem<T>::from_f32(0.f);
-    if (a.lse)
-      for (int i = threadIdx.x; i < a.Hq; i += NW * 32) a.lse[static_cast<int64_t>(b) * a.Hq + i] = -INFINITY;
-  }
+  auto zeros = [&]() {
+    for (int b = blockIdx.x; b < a.batch; b += n_cta) {
+      if (span_of(a, a.lens[b]).n > 0) continue;
+      for (int i = threadIdx.x; i < a.Hq * D; i += NW * 32)
+        static_cast<T*>(a.out)[static_cast<int64_t>(b) * a.Hq * D + i] = Elem<T>::from_f32(0.f);
+      if (a.lse)
+        for (int i = threadIdx.x; i < a.Hq; i += NW * 32) a.lse[static_cast<int64_t>(b) * a.Hq + i] = -INFINITY;
+    }
+  };
 
   // ---- items: the one in hand, and the producer's, NST blocks ahead ----
-  if (!next_item<KB>(a, &items[warp][0], sp, true)) return;     // the whole CTA
+  const bool some = a.fixed > 0 ? n_cta >= Hkv && fixed_item<KB>(a, &items[warp][0], blockIdx.x / Hkv, blockIdx.x % Hkv)
+                                : next_item<KB>(a, &items[warp][0], sp, true);
+  if (!some) {            // the whole CTA
+    zeros();
+    return;
+  }
   if (lane == 0) items[warp][1] = items[warp][0];
   __syncwarp();
   const Item& w = items[warp][0];
@@ -885,6 +916,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   settle();
   load_page();
   for (int s = 0; s < NST; ++s) issue();
+  zeros();               // while the first copies are on their way
 
   // ---- items ----
   int seq_c = 0;
@@ -1079,10 +1111,13 @@ int launch_attend(const CUtensorMap& map, const AttendArgs& a, void* scratch, in
   return with_kernel(dtype, d, e8, a.G, [&](auto kernel, int smem, int ctas, int KB) {
     // as many CTAs as fit the GPU, and no more than the longest sequences that the tables can name would take
     int64_t most = ctas * num_sms < kAttendRanges ? ctas * num_sms : kAttendRanges;
-    const int64_t blocks = ((static_cast<int64_t>(a.width) << a.pg.page_shift) + KB - 1) / KB;
+    int64_t blocks = ((static_cast<int64_t>(a.width) << a.pg.page_shift) + KB - 1) / KB;
+    if (a.window > 0 && a.window / KB + 2 < blocks) blocks = a.window / KB + 2;     // a window may begin and end inside a block
     const int64_t need = a.pg.Hkv * a.batch * ((blocks + kMinShare - 1) / kMinShare);
+    AttendArgs b = a;
+    b.fixed = need >= 1 && need <= most ? static_cast<int>((blocks + kMinShare - 1) / kMinShare) : 0;
     const int grid = static_cast<int>(need < 1 ? 1 : need < most ? need : most);
-    return launch_dependent(kernel, dim3(grid), NW * 32, smem, st, map, a, sc);
+    return launch_dependent(kernel, dim3(grid), NW * 32, smem, st, map, b, sc);
   });
 }
 

@@ -298,3 +298,34 @@ def test_attention_work_split(seed):
             assert (got[-1][1] if got else 0) == n
             assert all(x[2] == len(got) for x in got)
     assert read == written
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_attention_fixed_parts(seed):
+    """Narrow tables: parts of MIN_SHARE blocks, as many groups for each sequence as its longest would need."""
+    rng = np.random.default_rng(seed)
+    hkv, fixed, batch = int(rng.choice([1, 2, 8])), int(rng.integers(1, 9)), int(rng.integers(1, 9))
+    blocks = [int(x) for x in rng.integers(0, fixed * MIN_SHARE + 1, size=batch)]
+    n_cta = hkv * batch * fixed
+    cover, used = {}, set()
+    for cta in range(n_cta):
+        grp, h = divmod(cta, hkv)
+        b, part = divmod(grp, fixed)
+        if part * MIN_SHARE >= blocks[b]:
+            continue
+        parts, first = -(-blocks[b] // MIN_SHARE), grp - part
+        cover.setdefault((b, h), []).append((part * MIN_SHARE, min((part + 1) * MIN_SHARE, blocks[b])))
+        slot = 2 * (first + part) * hkv + h
+        assert slot not in used and slot < 2 * n_cta and len(cover[b, h]) <= parts
+        used.add(slot)
+    for b, n in enumerate(blocks):
+        for h in range(hkv):
+            got = sorted(cover.get((b, h), []))
+            assert [x[0] for x in got] == ([0] + [x[1] for x in got[:-1]])[:len(got)] and (got[-1][1] if got else 0) == n
+
+
+@pytest.mark.parametrize("kb", [8, 16, 32, 64])
+def test_blocks_of_a_window(kb):
+    """A window of w tokens touches at most w / kb + 2 blocks, wherever it ends."""
+    for w in range(1, 300):
+        assert max((n + kb - 1) // kb - max(n - w, 0) // kb for n in range(1, 400)) <= w // kb + 2
