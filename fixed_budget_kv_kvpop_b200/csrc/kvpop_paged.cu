@@ -587,7 +587,7 @@ int heads_t(const HeadsArgs& a, int mode, int num_sms, cudaStream_t st) {
 
 template <typename T, int D, bool E4M3>
 int gather_t(const GatherArgs& a, cudaStream_t st) {
-  const dim3 grid((a.n_tokens + kGatherTokens - 1) / kGatherTokens, a.pg.Hkv * 2, a.batch);
+  const dim3 grid((static_cast<unsigned>(a.n_tokens) + kGatherTokens - 1) / kGatherTokens, a.pg.Hkv * 2, a.batch);
   return launch_dependent(gather_kernel<T, D, E4M3>, grid, kThreads, 0, st, a);
 }
 

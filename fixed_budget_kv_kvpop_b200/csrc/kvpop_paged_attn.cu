@@ -4,18 +4,18 @@
 //
 // Work split.  The keys of a sequence are cut into blocks of KB.  CTAs work in
 // groups of Hkv, one for each KV head, so that the heads of a page, which are
-// neighbours in memory, are read at the same time (64 sequences of 8192 tokens
-// take 308 us so, and 328 us when CTAs take ranges of single heads wherever
-// they lie).  The groups either take one part of one sequence each, all parts
-// as even as they come, or, where that leaves the largest part well above the
-// average, equal contiguous ranges of all sequences' blocks.  Every CTA finds
-// its range from the lengths on the device.  Where the page table is so narrow
-// that even the longest sequences it can hold give no more parts of kMinShare
-// blocks than there are groups, those are the parts, and nothing is searched
-// for: short calls are a chain of latencies, of which the search was a third.  Where a sequence lies in several
-// ranges, each leaves a partial (accumulator, running maximum, sum), and the
-// CTA that arrives last joins them in their order, so results do not depend on
-// who is last.
+// neighbours in memory, are read at the same time.  The groups either take one
+// part of one sequence each, all parts as even as they come, or, where that
+// leaves the largest part well above the average, equal contiguous ranges of
+// all sequences' blocks (32 sequences of 16384 to 32768 tokens in 8 bits: 337
+// and 300 us; 16 of 8192 in fp32: 160 and 182 us).  Every CTA finds its range
+// from the lengths on the device.  Where the page table is so narrow that even
+// the longest sequences it can hold give no more parts of kMinShare blocks than
+// there are groups, those are the parts, and nothing is searched for: short
+// calls are a chain of latencies (117 tokens: 6.2 us so, 7.7 us searched).
+// Where a sequence lies in several ranges, each leaves a partial (accumulator,
+// running maximum, sum), and the CTA that arrives last joins them in their
+// order, so results do not depend on who is last.
 // Inside a CTA each warp has a ring of stages of its own: it copies block after
 // block into it by tensor copies (one instruction per 16 keys and values) and
 // computes on the oldest.  Warps meet once per item, to join their sums.
@@ -29,22 +29,7 @@ namespace kvpop {
 namespace {
 
 constexpr int NW = 4;                    // warps per CTA
-#ifndef KV_C4
-#define KV_C4 4
-#endif
-#ifndef KV_C8
-#define KV_C8 2
-#endif
-#ifndef KV_CE
-#define KV_CE 3
-#endif
-#ifndef KV_CF
-#define KV_CF 2
-#endif
-#ifndef KV_MIN
-#define KV_MIN 8
-#endif
-constexpr int kMinShare = KV_MIN;             // blocks of a part at least
+constexpr int kMinShare = 8;             // blocks of a part at least (1 x 1024 tokens: 4 12.9 us, 8 11.7 us, 16 12.4 us, 32 17.3 us)
 // Largest part that is taken for one part of one sequence per group, when equal
 // ranges would have `even` blocks: ranges cost a second item and its join.
 __host__ __device__ constexpr int64_t most_of(int64_t even) { return even + even / 5 + 16; }
@@ -241,7 +226,11 @@ struct Geo {
   static constexpr int SCALE = E4M3 ? NSUB * 128 : 0;        // bytes of scales of a stage
   static constexpr int MERGE = NW * GP * (D + 4) * 4;
   static constexpr int WEIGHTS = F32 ? NW * KEYS * 16 : 0;   // fp32: weights of a piece for four heads
-  static constexpr int CTAS = GP == 16 ? 2 : GP == 8 ? KV_C8 : F32 ? (D == 64 ? 3 : 2) : E4M3 ? KV_CE : KV_C4;    // per SM
+  // CTAs per SM.  More warps hide the chain from a block's arrival to its sums,
+  // up to where registers run out or power does: 64 x 8192 bf16 takes 338, 327
+  // and 314 us with 2, 3 and 4 CTAs in a short run, but 339, 336 and 359 us in
+  // a long one, where the GPU holds its 1000 W by its clock
+  static constexpr int CTAS = GP > 4 ? 2 : F32 ? (D == 64 ? 3 : 2) : 3;
   static constexpr int CTA = (228 * 1024) / CTAS - 1024;
   static constexpr int NST0 = (CTA - 1024 - MERGE - WEIGHTS - 512) / (NW * (STAGE + SCALE + 16));
   static constexpr int NST = NST0 > 8 ? 8 : NST0;

@@ -235,33 +235,40 @@ def test_e4m3_special_rows():
     assert (c.scales(0)[1, 0, 0, :2] == 0).all()
 
 
-@pytest.mark.parametrize("cache", ["native", "e4m3"])
-def test_append_qkv_is_heads_then_append(cache):
+@pytest.mark.parametrize("dtype,cache,d,hq,hkv,rot,inter,b,n", [
+    ("bf16", "native", 128, 8, 2, 128, False, 3, 21), ("bf16", "e4m3", 128, 8, 2, 128, False, 3, 21),
+    ("bf16", "e4m3", 64, 5, 5, 24, False, 2, 17), ("bf16", "e4m3", 128, 3, 1, 64, True, 1, 16),
+    ("bf16", "native", 64, 32, 8, 40, False, 16, 1), ("f32", "native", 128, 6, 3, 128, True, 2, 40),
+    ("f32", "native", 64, 4, 2, 24, False, 1, 900), ("bf16", "e4m3", 128, 64, 8, 96, False, 64, 1),
+])
+def test_append_qkv_is_heads_then_append(dtype, cache, d, hq, hkv, rot, inter, b, n):
     """Queries equal qk_norm_rope's bit for bit; native keys equal its keys; e4m3 keys are within half a step of the oracle's."""
-    b, n, hq, hkv, d, page = 3, 21, 8, 2, 128, 16
-    x = rows((b, n, hq + 2 * hkv, d), "bf16", 8)
+    page = 16
+    x = rows((b, n, hq + 2 * hkv, d), dtype, 8)
     q, k, v = x[:, :, :hq], x[:, :, hq:hq + hkv], x[:, :, hq + hkv:]
-    freq = 1e6 ** (-np.arange(0, d, 2) / d)
+    freq = 1e6 ** (-np.arange(0, rot, 2) / rot)
     kw = (1 + 0.1 * np.random.default_rng(0).normal(size=d)).astype(np.float32)
-    rope = kp.make_rope(torch.from_numpy(freq).cuda(), q_weight=torch.ones(d, device="cuda"), k_weight=torch.from_numpy(kw).cuda())
+    rope = kp.make_rope(torch.from_numpy(freq).cuda(), q_weight=torch.ones(d, device="cuda"), k_weight=torch.from_numpy(kw).cuda(),
+                        interleaved=inter)
     pos = np.arange(b * n, dtype=np.int32).reshape(b, n) * 1001
     table, n_pages = tables([n] * b, page)
     slots = slots_of(table, [n] * b, page, n)
-    slots[1, 15:] = -1
-    c = cache_of(hq, hkv, d, page, n_pages, cache=cache)
-    qo = torch.empty(b, n, hq, d, dtype=torch.bfloat16, device="cuda")
+    if n > 1:
+        slots[b // 2, n - 6:] = -1
+    c = cache_of(hq, hkv, d, page, n_pages, dtype=dtype, cache=cache)
+    qo = torch.empty(b, n, hq, d, dtype=TORCH[dtype], device="cuda")
     c.append_qkv(0, rope, q, k, v, ints(pos), ints(slots), qo)
-    q1, k1 = torch.empty_like(qo), torch.empty(b, n, hkv, d, dtype=torch.bfloat16, device="cuda")
+    q1, k1 = torch.empty_like(qo), torch.empty(b, n, hkv, d, dtype=TORCH[dtype], device="cuda")
     kp.qk_norm_rope(rope, q, k, ints(pos), q1, k1)
     assert torch.equal(qo, q1)
     if cache == "native":
-        check_held(c, 0, table, [n] * b, page, f64(k1), f64(v), slots, "bf16", cache)
+        check_held(c, 0, table, [n] * b, page, f64(k1), f64(v), slots, dtype, cache)
         return
     pages, scales = f64(c.pages(0).float()), f64(c.scales(0))
     for i in range(b):
         t = np.nonzero(slots[i] >= 0)[0]
         pg, r = slots[i, t] // page, slots[i, t] % page
-        want = po.heads(f64(k[i]), kw, 1e-6, pos[i], freq)[t]
+        want = po.heads(f64(k[i]), kw, 1e-6, pos[i], freq, interleaved=inter)[t]
         got = pages[pg, :, 0, r] * scales[pg, :, 0, r][..., None]
         top = np.abs(want).max(-1, keepdims=True)
         # half a step of e4m3 (relative 2^-4; 2^-10 of the scale where values are below 2^-6), keys off by 256 u of the row
@@ -269,7 +276,10 @@ def test_append_qkv_is_heads_then_append(cache):
         assert (np.abs(got - want) <= bound).all()
         wv, sv = po.hold_e4m3(f64(v[i])[t])
         np.testing.assert_array_equal(scales[pg, :, 1, r], sv)
-    assert (scales.transpose(0, 3, 1, 2)[table[1, 0], 15] == 0).all()   # padding wrote nothing
+        np.testing.assert_array_equal(pages[pg, :, 1, r], wv)
+    for i in range(b):                                              # padding wrote nothing
+        for t in np.nonzero(slots[i] < 0)[0]:
+            assert (scales[table[i, t // page], :, :, t % page] == 0).all()
 
 
 def test_bad_slots_and_pages_are_recorded():
@@ -441,6 +451,41 @@ def test_attend_long_and_many(dtype, cache, d, g, hkv, page):
         for i in range(0, b, max(1, b // 23)):
             x = held_rows(c, 0, table, lens[i], page, i)
             check_attend(out[i], lse[i], q[i], x[:, :, 0], x[:, :, 1], dtype)
+
+
+@pytest.mark.parametrize("dtype,cache,hq,hkv", [("bf16", "native", 600, 600), ("bf16", "e4m3", 460, 460), ("f32", "native", 500, 500),
+                                                 ("bf16", "native", 96, 6)])
+def test_attend_more_heads_than_the_gpu_has_blocks(dtype, cache, hq, hkv):
+    lens = [40, 0, 500, 17]
+    c, table, q = filled(lens, hq, hkv, 64, 16, dtype, cache, seed=2)
+    wide = np.full((4, 700), -1, np.int32)          # a wide table: nothing is known of the lengths beforehand
+    wide[:, :table.shape[1]] = table
+    out, lse, narrow = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda"), torch.empty_like(q)
+    c.attend(0, q, ints(wide), ints(lens), out, lse)
+    c.attend(0, q, ints(table), ints(lens), narrow)
+    for b, n in enumerate(lens):
+        x = held_rows(c, 0, table, n, 16, b)
+        check_attend(out[b], lse[b], q[b], x[:, :, 0], x[:, :, 1], dtype)
+        check_attend(narrow[b], None, q[b], x[:, :, 0], x[:, :, 1], dtype)
+    assert c.get_error() == (kp.KVPOP_OK, 0)
+
+
+@pytest.mark.parametrize("dtype,cache,d,g,hkv,page", [SHAPES[0], SHAPES[5], SHAPES[9], SHAPES[12]])
+@pytest.mark.parametrize("lens", [[1], [0], [3, 200, 0, 129], [700] * 20, [1, 2, 3] * 20, [5000, 4000, 3000, 10]])
+def test_attend_does_not_depend_on_the_table_s_width(dtype, cache, d, g, hkv, page, lens):
+    """Narrow tables fix the split beforehand, wide ones leave it to the lengths."""
+    c, table, q = filled(lens, g * hkv, hkv, d, page, dtype, cache, seed=13)
+    wide = np.full((len(lens), 4000), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    for t in (table[:, :max(1, -(-max(lens) // page))].copy(), wide):
+        for window in (0, 40):
+            out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+            if max(lens) == 0:
+                out.fill_(7), lse.fill_(7)
+            c.attend(0, q, ints(t), ints(lens), out, lse, window=window)
+            for b in range(0, len(lens), max(1, len(lens) // 7)):
+                x = held_rows(c, 0, table, lens[b], page, b)
+                check_attend(out[b], lse[b], q[b], x[:, :, 0], x[:, :, 1], dtype, window=window)
 
 
 def test_offsets_past_32_bits():
