@@ -253,7 +253,7 @@ __device__ __forceinline__ void write4(float* p, const float4& o, float L, bool 
   *reinterpret_cast<float4*>(p) = any ? make_float4(o.x / L, o.y / L, o.z / L, o.w / L) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-// One warp's part of a segment for bf16 and 8-bit rows: 16 keys a piece, on
+// One warp's part of an item for bf16 and 8-bit rows: 16 keys a piece, on
 // m16n8k16 matrix instructions.  S = Q K^T has the queries as rows (up to four
 // heads fill rows 0..3 and again 4..7), and its accumulator fragment, as
 // weights, is the B fragment of O^T += V^T P^T.  Weights go in as two bf16
@@ -270,6 +270,7 @@ struct MmaPieces {
   static constexpr int kD = D, kGP = GP;
   static constexpr int R = GP == 16 ? 2 : 1;      // query rows per lane
   static constexpr int KS = D / 16;               // 16-wide steps over the head
+  static constexpr int PK = G_::NSUB > 1 && GP < 16 ? 2 : 1;
   uint32_t qf[KS][4];
   float qmul[R];
   float acc[R][KS][4];
@@ -353,100 +354,106 @@ struct MmaPieces {
     }
   }
 
-  __device__ __forceinline__ void piece(const AttendArgs& a, uint8_t* kbase, const uint8_t* scales, int key0, int lo, int n, float*, bool& cleared) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const float qscale = a.scale * kLog2e;
-    (void)qscale;
+  // PK pieces at a time: twice the keys in the same chain of steps.  have: which of them were copied.
+  __device__ __forceinline__ void pieces(const AttendArgs& a, uint8_t* kbase, const uint8_t* scales, int key0, int lo, int n,
+                                         unsigned have, float*, bool& cleared) {
+    const int lane = threadIdx.x & 31, t = lane & 3;
     const uint32_t ks = smem_u32(kbase), vs = ks + G_::SUB / 2;
-    const bool part = key0 < lo || key0 + 16 > n;
+    const bool part = key0 < lo || key0 + 16 * PK > n || have != (1u << PK) - 1;
+    auto attended = [&](int i) { return key0 + i >= lo && key0 + i < n && ((have >> (i >> 4)) & 1); };
     if (part) {
       // values of tokens that are not attended: whatever they hold, weight zero must give zero
-      const int row = lane >> 1;
-      if (key0 + row < lo || key0 + row >= n) {
+#pragma unroll
+      for (int p = 0; p < PK; ++p) {
+        const int row = lane >> 1;
+        if (attended(16 * p + row)) continue;
         constexpr int CH = G_::ROWB / 16;
 #pragma unroll
         for (int hf = 0; hf < G_::HALVES; ++hf)
 #pragma unroll
           for (int c = 0; c < CH / 2; ++c)
-            *reinterpret_cast<uint4*>(kbase + G_::SUB / 2 + hf * 16 * G_::ROWB + row * G_::ROWB + ((lane & 1) * (CH / 2) + c) * 16) =
+            *reinterpret_cast<uint4*>(kbase + p * G_::SUB + G_::SUB / 2 + hf * 16 * G_::ROWB + row * G_::ROWB + ((lane & 1) * (CH / 2) + c) * 16) =
                 make_uint4(0, 0, 0, 0);
       }
       cleared = true;
       __syncwarp();
     }
-    // ---- scores: rows are queries, columns keys 0..7 and 8..15 ----
-    float s[2][2][4];
+    // ---- scores: rows are queries, columns eight keys for each nb; two chains of sums each for a single piece ----
+    constexpr int NB = 2 * PK, CHAINS = PK == 1 ? 2 : 1;
+    float s[NB][CHAINS][4];
 #pragma unroll
-    for (int nb = 0; nb < 2; ++nb)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < CHAINS; ++c)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[nb][c][i] = 0.f;
     if constexpr (!E4M3) {
 #pragma unroll
       for (int k = 0; k < KS / 2; ++k) {
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
+        for (int nb = 0; nb < NB; ++nb) {
           uint32_t f[4];
-          ldsm_x4(ks + kx[k & 1] + (k >> 1) * 2048 + nb * (8 * G_::ROWB), f);
+          ldsm_x4(ks + (nb >> 1) * G_::SUB + kx[k & 1] + (k >> 1) * 2048 + (nb & 1) * (8 * G_::ROWB), f);
           mma_bf16_16816(s[nb][0], qf[2 * k], f[0], f[1]);
-          mma_bf16_16816(s[nb][1], qf[2 * k + 1], f[2], f[3]);
+          mma_bf16_16816(s[nb][CHAINS - 1], qf[2 * k + 1], f[2], f[3]);
         }
       }
     } else {
 #pragma unroll
       for (int k = 0; k < KS / 4; ++k) {
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
+        for (int nb = 0; nb < NB; ++nb) {
           uint32_t f[4];
-          ldsm_x4(ks + kx[k & 1] + (k >> 1) * 2048 + nb * (8 * G_::ROWB), f);
+          ldsm_x4(ks + (nb >> 1) * G_::SUB + kx[k & 1] + (k >> 1) * 2048 + (nb & 1) * (8 * G_::ROWB), f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma_f16_16816(s[nb][i & 1], qf[4 * k + i], e4m3_to_f16(f[i]), e4m3_to_f16_high(f[i]));
+          for (int i = 0; i < 4; ++i)
+            mma_f16_16816(s[nb][i & (CHAINS - 1)], qf[4 * k + i], e4m3_to_f16(f[i]), e4m3_to_f16_high(f[i]));
         }
       }
     }
-    float2 kf[2], vf[2];
+    float2 kf[NB], vf[NB];
     if constexpr (E4M3) {
-      const float2* sp = reinterpret_cast<const float2*>(scales);
-      kf[0] = sp[t]; kf[1] = sp[4 + t]; vf[0] = sp[8 + t]; vf[1] = sp[12 + t];
-      if (part) {     // scales of tokens that are not attended may be anything
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb) {
-          const int key = key0 + nb * 8 + 2 * t;
-          if (key < lo || key >= n) vf[nb].x = 0.f;
-          if (key + 1 < lo || key + 1 >= n) vf[nb].y = 0.f;
+      for (int nb = 0; nb < NB; ++nb) {
+        const float2* sp = reinterpret_cast<const float2*>(scales + (nb >> 1) * 128) + (nb & 1) * 4 + t;
+        kf[nb] = sp[0]; vf[nb] = sp[8];
+        if (part) {     // scales of tokens that are not attended may be anything
+          if (!attended(nb * 8 + 2 * t)) vf[nb].x = 0.f;
+          if (!attended(nb * 8 + 2 * t + 1)) vf[nb].y = 0.f;
         }
       }
     }
-    uint32_t ph[R][2], pl[R][2];     // weights as two bf16 terms
-    float x[R][4];
+    uint32_t ph[R][NB], pl[R][NB];     // weights as two terms
+    float x[R][2 * NB];
     float top[R];
     bool raise = false;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float y = s[i >> 1][0][2 * r + (i & 1)] + s[i >> 1][1][2 * r + (i & 1)];
+      for (int i = 0; i < 2 * NB; ++i) {
+        float y = s[i >> 1][0][2 * r + (i & 1)];
+        if (CHAINS == 2) y += s[i >> 1][CHAINS - 1][2 * r + (i & 1)];
         if constexpr (E4M3) y *= (i & 1) ? kf[i >> 1].y : kf[i >> 1].x;
         x[r][i] = y * qmul[r];
       }
       if (a.softcap > 0.f) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[r][i] = a.softcap * kLog2e * tanhf(x[r][i] * (kLn2 / a.softcap));
+        for (int i = 0; i < 2 * NB; ++i) x[r][i] = a.softcap * kLog2e * tanhf(x[r][i] * (kLn2 / a.softcap));
       }
       if (part) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = key0 + (i >> 1) * 8 + 2 * t + (i & 1);
-          if (key < lo || key >= n) x[r][i] = -INFINITY;
-        }
+        for (int i = 0; i < 2 * NB; ++i)
+          if (!attended((i >> 1) * 8 + 2 * t + (i & 1))) x[r][i] = -INFINITY;
       }
-      top[r] = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
+      top[r] = x[r][0];
+#pragma unroll
+      for (int i = 1; i < 2 * NB; ++i) top[r] = fmaxf(top[r], x[r][i]);
       raise |= top[r] > m[r] + kRaise;
     }
     float vtop = 0.f;
     if constexpr (E4M3) {
-      vtop = fmaxf(fmaxf(vf[0].x, vf[0].y), fmaxf(vf[1].x, vf[1].y));
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) vtop = fmaxf(vtop, fmaxf(vf[nb].x, vf[nb].y));
       raise |= vtop >= 2.f * vref;
     }
     if (__any_sync(0xffffffffu, raise)) {
@@ -480,7 +487,7 @@ struct MmaPieces {
     for (int r = 0; r < R; ++r) {
       const float mu = m[r] == -INFINITY ? 0.f : m[r];
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) {
+      for (int nb = 0; nb < NB; ++nb) {
         float p0 = ex2(x[r][2 * nb] - mu), p1 = ex2(x[r][2 * nb + 1] - mu);
         l[r] += p0 + p1;
         if constexpr (E4M3) {
@@ -498,7 +505,7 @@ struct MmaPieces {
           lo = pack_bf16(p0 - hf.x, p1 - hf.y);
         }
         if (GP == 4) {
-          ph[r][nb] = g < 4 ? hi : lo;     // rows 4..7 repeat the heads: they carry the low terms
+          ph[r][nb] = lane < 16 ? hi : lo;     // rows 4..7 repeat the heads: they carry the low terms
         } else {
           ph[r][nb] = hi;
           pl[r][nb] = lo;
@@ -506,31 +513,34 @@ struct MmaPieces {
       }
     }
     // ---- accumulators += V^T P^T: rows are head elements, columns queries ----
-    if constexpr (!E4M3) {
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        uint32_t f[4];
-        ldsm_x4_t(vs + vx[k & 3] + (k >> 2) * 2048, f);
+    for (int p = 0; p < PK; ++p) {
+      if constexpr (!E4M3) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          mma_bf16_16816(acc[r][k], f, ph[r][0], ph[r][1]);
-          if (GP != 4) mma_bf16_16816(acc[r][k], f, pl[r][0], pl[r][1]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < KS; k += 2) {
-        uint32_t f[4];
-        ldsm_x4_t(vs + vx[k >> 1], f);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          // bytes: two keys' elements 2g, 2g + 1 -> the keys' pairs of element 2g (row g) and of 2g + 1 (row g + 8)
-          const uint32_t u = __byte_perm(f[2 * c], 0, 0x3120), w = __byte_perm(f[2 * c + 1], 0, 0x3120);
-          const uint32_t v[4] = {e4m3_to_f16(u), e4m3_to_f16_high(u), e4m3_to_f16(w), e4m3_to_f16_high(w)};
+        for (int k = 0; k < KS; ++k) {
+          uint32_t f[4];
+          ldsm_x4_t(vs + p * G_::SUB + vx[k & 3] + (k >> 2) * 2048, f);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            mma_f16_16816(acc[r][k + c], v, ph[r][0], ph[r][1]);
-            if (GP != 4) mma_f16_16816(acc[r][k + c], v, pl[r][0], pl[r][1]);
+            mma_bf16_16816(acc[r][k], f, ph[r][2 * p], ph[r][2 * p + 1]);
+            if (GP != 4) mma_bf16_16816(acc[r][k], f, pl[r][2 * p], pl[r][2 * p + 1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < KS; k += 2) {
+          uint32_t f[4];
+          ldsm_x4_t(vs + p * G_::SUB + vx[k >> 1], f);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            // bytes: two keys' elements 2g, 2g + 1 -> the keys' pairs of element 2g (row g) and of 2g + 1 (row g + 8)
+            const uint32_t u = __byte_perm(f[2 * c], 0, 0x3120), w = __byte_perm(f[2 * c + 1], 0, 0x3120);
+            const uint32_t v[4] = {e4m3_to_f16(u), e4m3_to_f16_high(u), e4m3_to_f16(w), e4m3_to_f16_high(w)};
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              mma_f16_16816(acc[r][k + c], v, ph[r][2 * p], ph[r][2 * p + 1]);
+              if (GP != 4) mma_f16_16816(acc[r][k + c], v, pl[r][2 * p], pl[r][2 * p + 1]);
+            }
           }
         }
       }
@@ -593,7 +603,7 @@ struct FmaPieces {
   static constexpr int kD = D, kGP = GP;
   static constexpr int NC = GP / 4;               // groups of four heads
   static constexpr int QV = D / 32, E = D / 32;   // float4s of a key's eighth; elements of a lane's accumulator
-  static constexpr int KEYS = G_::KEYS;
+  static constexpr int KEYS = G_::KEYS, PK = 1;
   const float* qbase;
   int heads;
   float4 q[4][QV];                                // of the group in hand
@@ -623,7 +633,7 @@ struct FmaPieces {
     if (NC == 1) load_q(0);
   }
 
-  __device__ __forceinline__ void piece(const AttendArgs& a, uint8_t* kbase, const uint8_t*, int key0, int lo, int n, float* wbuf, bool&) {
+  __device__ __forceinline__ void pieces(const AttendArgs& a, uint8_t* kbase, const uint8_t*, int key0, int lo, int n, unsigned, float* wbuf, bool&) {
     const int lane = threadIdx.x & 31, part = lane & 7, kg = lane >> 3;
     const float4* keys = reinterpret_cast<const float4*>(kbase);
     const float* values = reinterpret_cast<const float*>(kbase + G_::SUB / 2);
@@ -925,10 +935,11 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
       bool cleared = false;
       const unsigned have = dead ? 0u : static_cast<unsigned>(live[st]);
 #pragma unroll 1
-      for (int sub = 0; sub < NSUB; ++sub) {
-        if (!((have >> sub) & 1)) continue;
+      for (int sub = 0; sub < NSUB; sub += C::PK) {
+        const unsigned in_hand = (have >> sub) & ((1u << C::PK) - 1);
+        if (in_hand == 0) continue;
         any = true;
-        c.piece(a, ring + st * G_::STAGE + sub * G_::SUB, sring + st * G_::SCALE + sub * 128, j * KB + sub * G_::KEYS, lo, n, wbuf, cleared);
+        c.pieces(a, ring + st * G_::STAGE + sub * G_::SUB, sring + st * G_::SCALE + sub * 128, j * KB + sub * G_::KEYS, lo, n, in_hand, wbuf, cleared);
       }
       if (cleared) fence_proxy_async_smem();   // those stores come before the next copy into the stage
       __syncwarp();
