@@ -74,37 +74,39 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Attended tokens [lo, n) of a sequence whose length is given as n; lengths outside the table are cut.
-struct Span {
-  int lo, n;
-};
-__device__ __forceinline__ Span span_of(const AttendArgs& a, int n) {
-  const int64_t cap = static_cast<int64_t>(a.width) << a.pg.page_shift;
-  n = n < 0 ? 0 : n > cap ? static_cast<int>(cap) : n;
-  return Span{a.window > 0 && n > a.window ? n - a.window : 0, n};
-}
-
-// Blocks of sequence b.
-template <int KB>
-__device__ __forceinline__ int blocks_of(const AttendArgs& a, int b) {
-  const Span s = span_of(a, a.lens[b]);
-  return (s.n + KB - 1) / KB - s.lo / KB;
-}
-
 // a / b for a >= 0, b > 0: in 32 bits where a allows, a fraction of the 64-bit division's time.
 __device__ __forceinline__ int64_t quotient(int64_t a, int b) {
   if ((a >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
   return a / b;
 }
 
-// How the work is split; the same in every warp of the launch.
+// The sequences and how their work is split.  Kept in shared memory, one copy
+// per warp: the function that finds items reads it from there, where an
+// argument struct passed on by address costs a trip to global memory.
 struct Split {
+  const int32_t* lens;
   int64_t total;     // blocks of all sequences
+  int batch, Hkv, window, fixed;   // as AttendArgs
+  int cap;           // tokens that a row of the page table can name
   int share;         // blocks of a range
   int groups;        // groups of CTAs
-  int nb0;           // blocks of sequence `lane`
-  bool aligned;      // one part of one sequence per group
+  int aligned;       // one part of one sequence per group
 };
+
+// Attended tokens [lo, n) of a sequence whose length is given as n; lengths outside the table are cut.
+struct Span {
+  int lo, n;
+};
+__device__ __forceinline__ Span span_of(const Split& sp, int n) {
+  n = n < 0 ? 0 : min(n, sp.cap);
+  return Span{sp.window > 0 && n > sp.window ? n - sp.window : 0, n};
+}
+// Blocks of sequence b.
+template <int KB>
+__device__ __forceinline__ int blocks_of(const Split& sp, int b) {
+  const Span s = span_of(sp, sp.lens[b]);
+  return (s.n + KB - 1) / KB - s.lo / KB;
+}
 
 // An item: blocks of one sequence and head.  Each warp keeps two in shared
 // memory, the one it computes on and the one it copies for, so that they take
@@ -121,9 +123,9 @@ struct Item {
 
 // The item of a group where parts are fixed: kMinShare blocks of one sequence.
 template <int KB>
-__device__ __forceinline__ bool fixed_item(const AttendArgs& a, Item* it, int grp, int h) {
-  const int b = grp / a.fixed, part = grp - b * a.fixed;
-  const Span s = span_of(a, a.lens[b]);
+__device__ __forceinline__ bool fixed_item(const Split& sp, Item* it, int grp, int h) {
+  const int b = grp / sp.fixed, part = grp - b * sp.fixed;
+  const Span s = span_of(sp, sp.lens[b]);
   const int j0 = s.lo / KB, nb = (s.n + KB - 1) / KB - j0;
   if (part * kMinShare >= nb) return false;
   __syncwarp();
@@ -136,34 +138,36 @@ __device__ __forceinline__ bool fixed_item(const AttendArgs& a, Item* it, int gr
 }
 
 // The CTA's first or next item (the whole warp together); false at the end.
-// CTAs take one head, or with more heads than CTAs every gridDim.x-th.
+// CTAs take one head, or with more heads than CTAs every gridDim.x-th.  nb0:
+// blocks of sequence `lane`.
 template <int KB>
-__device__ __noinline__ bool next_item(const AttendArgs& a, Item* it, const Split& sp, bool start) {
-  const int lane = threadIdx.x & 31, Hkv = a.pg.Hkv, n_cta = gridDim.x;
+__device__ __noinline__ bool next_item(const Split* spp, Item* it, int nb0, bool start) {
+  const Split& sp = *spp;
+  const int lane = threadIdx.x & 31, Hkv = sp.Hkv, n_cta = gridDim.x;
   const bool many = Hkv > n_cta;
   const int grp = many ? 0 : static_cast<int>(blockIdx.x) / Hkv;
-  int b = 0, h, part = 0, parts = 1, skip = 0, left;
+  int b = 0, h, parts = 1, skip = 0, left;
   int64_t pos = 0;
   if (!start && it->left > it->jend - it->j) {       // the range goes on in the next sequence that has blocks
     h = it->h;
     left = it->left - (it->jend - it->j);
     pos = it->pos + (it->jend - it->j);
     b = it->b;
-    do ++b; while (blocks_of<KB>(a, b) == 0);
+    do ++b; while (blocks_of<KB>(sp, b) == 0);
   } else {
     h = start ? (many ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) - grp * Hkv) : it->h + n_cta;
     if (h >= Hkv || grp >= sp.groups) return false;
-    if (a.fixed > 0) return fixed_item<KB>(a, it, grp, h);
+    if (sp.fixed > 0) return fixed_item<KB>(sp, it, grp, h);
     // the sequence in which the range begins
     const int64_t target = sp.aligned ? grp : static_cast<int64_t>(grp) * sp.share;
     int64_t before = 0;
     for (int b0 = 0;; b0 += 32) {
-      if (b0 >= a.batch) return false;
-      int nb = 0;
-      if (b0 + lane < a.batch) nb = b0 == 0 ? sp.nb0 : blocks_of<KB>(a, b0 + lane);
-      const int own = sp.aligned ? (nb + sp.share - 1) / sp.share : nb;
+      if (b0 >= sp.batch) return false;
+      int own = 0;
+      if (b0 + lane < sp.batch) own = b0 == 0 ? nb0 : blocks_of<KB>(sp, b0 + lane);
+      if (sp.aligned) own = static_cast<int>(static_cast<uint32_t>(own + sp.share - 1) / static_cast<uint32_t>(sp.share));
       uint32_t sum = own;            // 32 sequences of at most 2^26 blocks
-      if (a.batch > 1) {
+      if (sp.batch > 1) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
@@ -180,21 +184,20 @@ __device__ __noinline__ bool next_item(const AttendArgs& a, Item* it, const Spli
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
     }
-    part = skip;
     pos = target;
     left = static_cast<int>(min(static_cast<int64_t>(sp.share), sp.total - target));
   }
   __syncwarp();                      // the old item has been read
   if (lane == 0) {
-    const Span s = span_of(a, a.lens[b]);
+    const Span s = span_of(sp, sp.lens[b]);
     const int j0 = s.lo / KB, nb = (s.n + KB - 1) / KB - j0;
     Item x;
     x.b = b; x.h = h; x.lo = s.lo; x.n = s.n; x.pos = pos;
-    if (sp.aligned) {
-      x.j = j0 + static_cast<int>(quotient(static_cast<int64_t>(nb) * part, parts));
-      x.jend = j0 + static_cast<int>(quotient(static_cast<int64_t>(nb) * (part + 1), parts));
+    if (sp.aligned) {                // part `skip`
+      x.j = j0 + static_cast<int>(quotient(static_cast<int64_t>(nb) * skip, parts));
+      x.jend = j0 + static_cast<int>(quotient(static_cast<int64_t>(nb) * (skip + 1), parts));
       x.left = x.jend - x.j;
-      x.first = grp - part; x.parts = parts; x.second = 0;
+      x.first = grp - skip; x.parts = parts; x.second = 0;
     } else {
       x.j = j0 + skip;
       x.jend = min(j0 + nb, x.j + left);
@@ -240,6 +243,11 @@ struct Geo {
 
 // A range begins in one sequence and ends in another, so a group leaves at
 // most two partials per head: that of its range's first sequence, and another.
+// Partial i of an item's sequence: by group, and whether its range begins with this sequence.
+__device__ __forceinline__ int64_t slot_of(const Item& x, int i, int Hkv) {
+  return static_cast<int64_t>(2 * (x.first + i) + (i == 0 ? x.second : 0)) * Hkv + x.h;
+}
+
 struct AttendScratch {
   float* acc;        // [2 kAttendRanges][G][D]
   float* ml;         // [2 kAttendRanges][G][4]: running maximum, sum, whether any key was seen
@@ -766,8 +774,9 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   uint64_t* bars = reinterpret_cast<uint64_t*>(mml + NW * GP * 4) + warp * NST;
   int32_t* live = reinterpret_cast<int32_t*>(reinterpret_cast<uint64_t*>(mml + NW * GP * 4) + NW * NST) + warp * NST;
   float* wbuf = reinterpret_cast<float*>(smem + G_::SMEM - 1024 - 256 - G_::WEIGHTS) + warp * (G_::WEIGHTS / (4 * NW));
-  __shared__ int last_flag;
-  __shared__ Item items[NW][2];
+  __shared__ int last_[2];
+  __shared__ Item items[NW][2], open_[2];
+  __shared__ Split split_[NW];
 
   if (lane == 0) {
     if (!G_::F32) asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map)) : "memory");
@@ -780,11 +789,17 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   // ---- the split ----
   const int Hkv = a.pg.Hkv, G = a.G, n_cta = gridDim.x;
   Split sp;
+  sp.lens = a.lens;
+  sp.batch = a.batch; sp.Hkv = Hkv; sp.window = a.window; sp.fixed = a.fixed;
+  sp.cap = static_cast<int>(min(static_cast<int64_t>(a.width) << a.pg.page_shift, static_cast<int64_t>(1 << 30)));
   sp.groups = max(1, n_cta / Hkv);
+  sp.total = 0; sp.share = kMinShare; sp.aligned = 0;
+  int nb0 = 0;             // blocks of sequence `lane`
   if (a.fixed > 0) {
-    sp.aligned = true;
-    if (warp == 0 && lane == 0 && blockIdx.x < a.batch && a.lens[blockIdx.x] != span_of(a, a.lens[blockIdx.x]).n)
-      set_error(a.pg.err, DEVERR_BAD_INDEX);
+    if (warp == 0 && lane == 0 && blockIdx.x < a.batch) {
+      const int given = a.lens[blockIdx.x];
+      if (given != span_of(sp, given).n) set_error(a.pg.err, DEVERR_BAD_INDEX);
+    }
   } else {
     int64_t total = 0;
     int longest = 0, seqs = 0;
@@ -794,11 +809,11 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
       int nb = 0;
       if (b < a.batch) {
         const int given = a.lens[b];
-        const Span s = span_of(a, given);
+        const Span s = span_of(sp, given);
         nb = (s.n + KB - 1) / KB - s.lo / KB;
         bad_len |= given != s.n;
       }
-      if (b0 == 0) sp.nb0 = nb;
+      if (b0 == 0) nb0 = nb;
       total += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(nb));     // 32 sequences of at most 2^26 blocks
       longest = max(longest, __reduce_max_sync(0xffffffffu, nb));
       seqs += __popc(__ballot_sync(0xffffffffu, nb > 0));
@@ -807,14 +822,14 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
     sp.total = total;
     const int64_t even = quotient(total + sp.groups - 1, sp.groups);
     sp.share = static_cast<int>(min(max(even, static_cast<int64_t>(kMinShare)), static_cast<int64_t>(1 << 30)));
-    sp.aligned = false;
     if (seqs > 0 && seqs <= sp.groups) {
       // the smallest largest part with which there are no more parts than groups
       auto fits = [&](int s) {
         int items = 0;
         for (int b0 = 0; b0 < a.batch; b0 += 32) {
-          int np = 0;
-          if (b0 + lane < a.batch) np = ((b0 == 0 ? sp.nb0 : blocks_of<KB>(a, b0 + lane)) + s - 1) / s;
+          int nb = 0;
+          if (b0 + lane < a.batch) nb = b0 == 0 ? nb0 : blocks_of<KB>(sp, b0 + lane);
+          const int np = static_cast<int>(static_cast<uint32_t>(nb + s - 1) / static_cast<uint32_t>(s));
           items += __reduce_add_sync(0xffffffffu, min(np, sp.groups + 1));
         }
         return items <= sp.groups;
@@ -831,16 +846,19 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
         }
       }
       if (hi <= most_of(sp.share)) {
-        sp.aligned = true;
+        sp.aligned = 1;
         sp.share = hi;
       }
     }
   }
+  if (lane == 0) split_[warp] = sp;
+  __syncwarp();
+  const Split* const spp = &split_[warp];
 
   // sequences without a token
   auto zeros = [&]() {
     for (int b = blockIdx.x; b < a.batch; b += n_cta) {
-      if (span_of(a, a.lens[b]).n > 0) continue;
+      if (span_of(*spp, a.lens[b]).n > 0) continue;
       for (int i = threadIdx.x; i < a.Hq * D; i += NW * 32)
         static_cast<T*>(a.out)[static_cast<int64_t>(b) * a.Hq * D + i] = Elem<T>::from_f32(0.f);
       if (a.lse)
@@ -849,8 +867,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   };
 
   // ---- items: the one in hand, and the producer's, NST blocks ahead ----
-  const bool some = a.fixed > 0 ? n_cta >= Hkv && fixed_item<KB>(a, &items[warp][0], blockIdx.x / Hkv, blockIdx.x % Hkv)
-                                : next_item<KB>(a, &items[warp][0], sp, true);
+  const bool some = a.fixed > 0 ? n_cta >= Hkv && fixed_item<KB>(sp, &items[warp][0], blockIdx.x / Hkv, blockIdx.x % Hkv)
+                                : next_item<KB>(spp, &items[warp][0], nb0, true);
   if (!some) {            // the whole CTA
     zeros();
     return;
@@ -866,7 +884,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   int pj = first_own(p.j), p_end = p.jend, seq_p = 0, page_next = -2;
   auto settle = [&]() {  // moves p to an item that has a block for this warp
     while (p_more && pj >= p_end) {
-      p_more = next_item<KB>(a, &p, sp, false);
+      p_more = next_item<KB>(spp, &p, nb0, false);
       pj = first_own(p.j);
       p_end = p.jend;
     }
@@ -918,6 +936,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   zeros();               // while the first copies are on their way
 
   // ---- items ----
+  int n_open = 0;          // items that are parts of their sequence
   int seq_c = 0;
   for (bool more = true; more;) {
     C c;
@@ -953,10 +972,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
     c.close(macc, mml, warp, any);
     __syncthreads();
     const bool complete = w.parts == 1;
-    const int64_t unit = static_cast<int64_t>(w.b) * Hkv + w.h;
-    // partial i of the sequence: by group, and whether its range begins with this sequence
-    auto slot_of = [&](int i) { return (2 * (w.first + i) + (i == 0 ? w.second : 0)) * Hkv + w.h; };
-    const int slot = complete ? 0 : slot_of(static_cast<int>(blockIdx.x) / Hkv - w.first);
+    const int64_t slot = complete ? 0 : slot_of(w, static_cast<int>(blockIdx.x) / Hkv - w.first, Hkv);
     const int64_t orow = static_cast<int64_t>(w.b) * a.Hq + static_cast<int64_t>(w.h) * G;
     for (int i = threadIdx.x; i < G * (D / 4); i += NW * 32) {
       const int q = i / (D / 4), e = (i % (D / 4)) * 4;
@@ -981,57 +997,70 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
         write4(static_cast<T*>(a.out) + (orow + q) * D + e, o, L, seen > 0.f);
         if (a.lse && e == 0) a.lse[orow + q] = seen > 0.f ? (mu + log2f(L)) * kLn2 : -INFINITY;
       } else {
-        __stcg(reinterpret_cast<float4*>(sc.acc + (static_cast<int64_t>(slot) * G + q) * D + e), o);
-        if (e == 0) __stcg(reinterpret_cast<float4*>(sc.ml + (static_cast<int64_t>(slot) * G + q) * 4), make_float4(M, L, seen, 0.f));
+        __stcg(reinterpret_cast<float4*>(sc.acc + (slot * G + q) * D + e), o);
+        if (e == 0) __stcg(reinterpret_cast<float4*>(sc.ml + (slot * G + q) * 4), make_float4(M, L, seen, 0.f));
       }
     }
     if (!complete) {
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) last_flag = atomicAdd(&sc.ticket[unit], 1) == w.parts - 1;
-      __syncthreads();
-      if (last_flag) {
-        __threadfence();
-        if (threadIdx.x == 0) sc.ticket[unit] = 0;
-        for (int i = threadIdx.x; i < G * (D / 4); i += NW * 32) {
-          const int q = i / (D / 4), e = (i % (D / 4)) * 4;
-          float M = -INFINITY, L = 0.f, seen = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          constexpr int PB = 8;          // partials on their way at a time
-          for (int c0 = 0; c0 < w.parts; c0 += PB) {
-            float4 ml[PB], v[PB];
-#pragma unroll
-            for (int c = 0; c < PB; ++c) {
-              ml[c] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-              if (c0 + c < w.parts) {
-                const int64_t sl = static_cast<int64_t>(slot_of(c0 + c)) * G + q;
-                ml[c] = __ldcg(reinterpret_cast<const float4*>(sc.ml + sl * 4));
-                v[c] = __ldcg(reinterpret_cast<const float4*>(sc.acc + sl * D + e));
-              }
-            }
-            float M1 = M;
-#pragma unroll
-            for (int c = 0; c < PB; ++c) M1 = fmaxf(M1, ml[c].x);
-            const float mu = M1 == -INFINITY ? 0.f : M1, ca = ex2(M - mu);
-            M = M1;
-            L *= ca; o.x *= ca; o.y *= ca; o.z *= ca; o.w *= ca;
-#pragma unroll
-            for (int c = 0; c < PB; ++c) {
-              if (ml[c].z == 0.f) continue;      // no key in that part
-              const float cb = ex2(ml[c].x - mu);
-              seen += ml[c].z;
-              L = fmaf(cb, ml[c].y, L);
-              o.x = fmaf(cb, v[c].x, o.x); o.y = fmaf(cb, v[c].y, o.y);
-              o.z = fmaf(cb, v[c].z, o.z); o.w = fmaf(cb, v[c].w, o.w);
-            }
-          }
-          write4(static_cast<T*>(a.out) + (orow + q) * D + e, o, L, seen > 0.f);
-          if (a.lse && e == 0) a.lse[orow + q] = seen > 0.f ? ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2 : -INFINITY;
-        }
-      }
+      if (threadIdx.x == 0) open_[n_open] = w;
+      ++n_open;
     }
     __syncthreads();     // the join's buffers are free again
-    more = next_item<KB>(a, &items[warp][0], sp, false);
+    more = next_item<KB>(spp, &items[warp][0], nb0, false);
+  }
+  // ---- sequences that lie in other ranges too (the range's first and last): join them if all parts are there ----
+  // Left for the end, since each step waits for the one before at the far side of L2, 2 us and more while the
+  // GPU reads at full speed.
+  if (n_open > 0) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x < n_open) {
+      const Item& x = open_[threadIdx.x];
+      last_[threadIdx.x] = atomicAdd(&sc.ticket[static_cast<int64_t>(x.b) * Hkv + x.h], 1) == x.parts - 1;
+    }
+    __syncthreads();
+    for (int i_open = 0; i_open < n_open; ++i_open) {
+      if (!last_[i_open]) continue;
+      const Item& x = open_[i_open];
+      const int64_t orow = static_cast<int64_t>(x.b) * a.Hq + static_cast<int64_t>(x.h) * G;
+      __threadfence();
+      if (threadIdx.x == 0) sc.ticket[static_cast<int64_t>(x.b) * Hkv + x.h] = 0;
+      for (int i = threadIdx.x; i < G * (D / 4); i += NW * 32) {
+        const int q = i / (D / 4), e = (i % (D / 4)) * 4;
+        float M = -INFINITY, L = 0.f, seen = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int PB = 8;          // partials on their way at a time
+        for (int c0 = 0; c0 < x.parts; c0 += PB) {
+          float4 ml[PB], v[PB];
+#pragma unroll
+          for (int c = 0; c < PB; ++c) {
+            ml[c] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+            if (c0 + c < x.parts) {
+              const int64_t sl = slot_of(x, c0 + c, Hkv) * G + q;
+              ml[c] = __ldcg(reinterpret_cast<const float4*>(sc.ml + sl * 4));
+              v[c] = __ldcg(reinterpret_cast<const float4*>(sc.acc + sl * D + e));
+            }
+          }
+          float M1 = M;
+#pragma unroll
+          for (int c = 0; c < PB; ++c) M1 = fmaxf(M1, ml[c].x);
+          const float mu = M1 == -INFINITY ? 0.f : M1, ca = ex2(M - mu);
+          M = M1;
+          L *= ca; o.x *= ca; o.y *= ca; o.z *= ca; o.w *= ca;
+#pragma unroll
+          for (int c = 0; c < PB; ++c) {
+            if (ml[c].z == 0.f) continue;      // no key in that part
+            const float cb = ex2(ml[c].x - mu);
+            seen += ml[c].z;
+            L = fmaf(cb, ml[c].y, L);
+            o.x = fmaf(cb, v[c].x, o.x); o.y = fmaf(cb, v[c].y, o.y);
+            o.z = fmaf(cb, v[c].z, o.z); o.w = fmaf(cb, v[c].w, o.w);
+          }
+        }
+        write4(static_cast<T*>(a.out) + (orow + q) * D + e, o, L, seen > 0.f);
+        if (a.lse && e == 0) a.lse[orow + q] = seen > 0.f ? ((M == -INFINITY ? 0.f : M) + log2f(L)) * kLn2 : -INFINITY;
+      }
+    }
   }
   // copies that a dead warp leaves in flight: wait for them (bounded) before its shared memory goes
   if (dead)
