@@ -410,9 +410,10 @@ constexpr int heads_smem() { return (kThreads / 32) * ((sizeof(T) == 2 ? 6 : 4) 
 // token's keys or values (blockIdx.y: which, and which `chunk` of their
 // passes), RPW rows a pass, U passes on their way at a time.  Rows that are
 // only copied take d / 8 lanes (16 bytes each in bf16), rows that are
-// quantised d / 16, which halves the exchanges and reciprocals per row.
+// quantised d / 16, which halves the exchanges and reciprocals per row.  Five
+// blocks per SM: 65536 tokens to 8 bits take 76.8 us, 80.6 with four, 77.7 with six.
 template <typename T, int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ HeadsArgs a, int passes, int chunk) {
+__global__ void __launch_bounds__(kThreads, 5) append_kernel(const __grid_constant__ HeadsArgs a, int passes, int chunk) {
   constexpr int LPR = E4M3 ? D / 16 : D / 8, RPW = 32 / LPR, U = E4M3 ? 2 : 4;
   wait_for_prior_kernel();
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;

@@ -194,8 +194,8 @@ __device__ __noinline__ bool next_item(const Split* spp, Item* it, int nb0, bool
     Item x;
     x.b = b; x.h = h; x.lo = s.lo; x.n = s.n; x.pos = pos;
     if (sp.aligned) {                // part `skip`
-      x.j = j0 + static_cast<int>(quotient(static_cast<int64_t>(nb) * skip, parts));
-      x.jend = j0 + static_cast<int>(quotient(static_cast<int64_t>(nb) * (skip + 1), parts));
+      x.j = j0 + skip * sp.share;
+      x.jend = min(x.j + sp.share, j0 + nb);
       x.left = x.jend - x.j;
       x.first = grp - skip; x.parts = parts; x.second = 0;
     } else {
@@ -795,6 +795,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   sp.groups = max(1, n_cta / Hkv);
   sp.total = 0; sp.share = kMinShare; sp.aligned = 0;
   int nb0 = 0;             // blocks of sequence `lane`
+  Span span0{0, 0};        // and its tokens
   if (a.fixed > 0) {
     if (warp == 0 && lane == 0 && blockIdx.x < a.batch) {
       const int given = a.lens[blockIdx.x];
@@ -807,13 +808,17 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
       const int b = b0 + lane;
       int nb = 0;
+      Span s{0, 0};
       if (b < a.batch) {
         const int given = a.lens[b];
-        const Span s = span_of(sp, given);
+        s = span_of(sp, given);
         nb = (s.n + KB - 1) / KB - s.lo / KB;
         bad_len |= given != s.n;
       }
-      if (b0 == 0) nb0 = nb;
+      if (b0 == 0) {
+        nb0 = nb;
+        span0 = s;
+      }
       total += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(nb));     // 32 sequences of at most 2^26 blocks
       longest = max(longest, __reduce_max_sync(0xffffffffu, nb));
       seqs += __popc(__ballot_sync(0xffffffffu, nb > 0));
@@ -867,8 +872,31 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   };
 
   // ---- items: the one in hand, and the producer's, NST blocks ahead ----
-  const bool some = a.fixed > 0 ? n_cta >= Hkv && fixed_item<KB>(sp, &items[warp][0], blockIdx.x / Hkv, blockIdx.x % Hkv)
-                                : next_item<KB>(spp, &items[warp][0], nb0, true);
+  bool some;
+  if (a.fixed > 0) {
+    some = n_cta >= Hkv && fixed_item<KB>(sp, &items[warp][0], blockIdx.x / Hkv, blockIdx.x % Hkv);
+  } else if (sp.aligned && a.batch <= 32 && n_cta >= Hkv) {
+    // what next_item does, from what the lanes already have
+    const int grp = blockIdx.x / Hkv;
+    const int own = static_cast<int>(static_cast<uint32_t>(nb0 + sp.share - 1) / static_cast<uint32_t>(sp.share));
+    int sum = own;
+    if (a.batch > 1) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
+      }
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, sum > grp);
+    some = past != 0 && grp < sp.groups;
+    if (some && lane == __ffs(past) - 1) {
+      const int part = grp - (sum - own), j0 = span0.lo / KB, j = j0 + part * sp.share, jend = min(j + sp.share, j0 + nb0);
+      items[warp][0] = Item{lane, static_cast<int>(blockIdx.x) - grp * Hkv, span0.lo, span0.n, j, jend, grp - part, own, 0, jend - j, 0};
+    }
+    __syncwarp();
+  } else {
+    some = next_item<KB>(spp, &items[warp][0], nb0, true);
+  }
   if (!some) {            // the whole CTA
     zeros();
     return;

@@ -242,7 +242,7 @@ def _items(cta, blocks, hkv, n_cta, share, groups, aligned):
             return out
         skip = target - before
         if aligned:
-            out.append((b, h, n * skip // own, n * (skip + 1) // own, grp - skip, own, 0))
+            out.append((b, h, skip * share, min((skip + 1) * share, n), grp - skip, own, 0))
             continue
         pos, left = target, min(share, sum(blocks) - target)
         while True:
