@@ -909,7 +909,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   auto first_own = [&](int j) { return j + ((warp - j) & (NW - 1)); };
   bool dead = false;     // a wait ran out: nothing more is copied or computed
   bool p_more = true;
-  int pj = first_own(p.j), p_end = p.jend, seq_p = 0, page_next = -2;
+  int pj = first_own(p.j), p_end = p.jend, seq_p = 0, page_next = -1;
+  bool page_want = false;
   auto settle = [&]() {  // moves p to an item that has a block for this warp
     while (p_more && pj >= p_end) {
       p_more = next_item<KB>(spp, &p, nb0, false);
@@ -918,19 +919,15 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
     }
   };
   auto load_page = [&]() {   // lane i: the page of piece i of the next block
-    page_next = -2;
-    if (p_more && lane < NSUB) {
-      const int key = pj * KB + lane * G_::KEYS;
-      if (key < p.n && key + G_::KEYS > p.lo)
-        page_next = a.table[p.b * a.table_stride + (key >> a.pg.page_shift)];
-    }
+    const int key = pj * KB + lane * G_::KEYS;
+    page_want = p_more && lane < NSUB && key < p.n && key + G_::KEYS > p.lo;
+    if (page_want) page_next = a.table[p.b * a.table_stride + (key >> a.pg.page_shift)];
   };
   auto issue = [&]() {
     if (!p_more || dead) return;
     const int st = seq_p % NST;
-    const bool want = page_next != -2;
-    const bool ok = want && page_next >= 0 && page_next < a.pg.n_pages;
-    if (want && !ok) set_error(a.pg.err, DEVERR_BAD_INDEX);
+    const bool ok = page_want && page_next >= 0 && page_next < a.pg.n_pages;
+    if (page_want && !ok) set_error(a.pg.err, DEVERR_BAD_INDEX);
     const unsigned m = __ballot_sync(0xffffffffu, ok);
     if (lane == 0) {
       live[st] = static_cast<int32_t>(m);

@@ -310,6 +310,34 @@ def test_bad_slots_and_pages_are_recorded():
         assert torch.equal(ko[b, :n], k[0, :n]) and (ko[b, n:] == 2).all() and (vo[b, n:] == 2).all()
 
 
+@pytest.mark.parametrize("bad", [-1, -2, -2 ** 31, 7, 2 ** 31 - 1])
+@pytest.mark.parametrize("dtype,cache,page", [("bf16", "native", 16), ("bf16", "e4m3", 16), ("f32", "native", 32)])
+def test_every_bad_page_is_recorded(bad, dtype, cache, page):
+    """One bad entry among good ones: recorded, its tokens left out of the sum and of what is read back."""
+    n = 5 * page - 3
+    c = cache_of(4, 2, 64, page, 7, dtype, cache)
+    k = rows((1, n, 2, 64), dtype, 1)
+    table = np.array([[6, 0, 4, 2, 5]], np.int32)
+    c.append(0, k, k, ints(slots_of(table, [n], page, n)))
+    q = rows((1, 4, 64), dtype, 2)
+    x = held_rows(c, 0, table, n, page, 0)
+    for at in (0, 2, 4):
+        t = table.copy()
+        t[0, at] = bad
+        out = torch.empty_like(q)
+        c.attend(0, q, ints(t), ints([n]), out)
+        assert c.get_error() == (kp.KVPOP_ERR_DEVICE, kp.KVPOP_DEVERR_BAD_INDEX)
+        c.clear_error()
+        keep = np.r_[0:at * page, min((at + 1) * page, n):n]
+        check_attend(out[0], None, q[0], x[keep, :, 0], x[keep, :, 1], dtype)
+        ko, vo = (torch.full((1, n, 2, 64), 9.0, dtype=TORCH[dtype], device="cuda") for _ in range(2))
+        c.gather(0, ints(t), ints([n]), ko, vo)
+        assert c.get_error() == (kp.KVPOP_ERR_DEVICE, kp.KVPOP_DEVERR_BAD_INDEX)
+        c.clear_error()
+        gone = slice(at * page, min((at + 1) * page, n))
+        assert (ko[0, gone] == 9).all() and (vo[0, gone] == 9).all() and not (ko[0, keep] == 9).all(-1).any()
+
+
 # ---- attend ----
 
 def check_attend(out, lse, q, k, v, dtype, scale=None, softcap=0.0, window=0):
