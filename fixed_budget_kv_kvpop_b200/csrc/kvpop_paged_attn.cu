@@ -13,6 +13,8 @@
 // the longest sequences it can hold give no more parts of kMinShare blocks than
 // there are groups, those are the parts, and nothing is searched for: short
 // calls are a chain of latencies (117 tokens: 6.2 us so, 7.7 us searched).
+// Many sequences of a few blocks each go, head by head, to single warps, which
+// then meet nobody (512 of 60 tokens: 38 us so, 71 us with a CTA for each).
 // Where a sequence lies in several ranges, each leaves a partial (accumulator,
 // running maximum, sum), and the CTA that arrives last joins them in their
 // order, so results do not depend on who is last.
@@ -30,6 +32,11 @@ namespace {
 
 constexpr int NW = 4;                    // warps per CTA
 constexpr int kMinShare = 8;             // blocks of a part at least (1 x 1024 tokens: 4 12.9 us, 8 11.7 us, 16 12.4 us, 32 17.3 us)
+// If there are more sequences than groups and none has more tokens than this, they go to single warps.  Few long ones
+// would leave warps idle (8 groups of 4 heads, bf16: 64 x 200 19 us against 25, 64 x 300 27 either way, 256 x 300 69
+// against 66; e4m3 64 x 400 34 against 30), the sooner the more a warp has to compute (fp32 on the FMA units, 8 groups
+// of 16 heads: 80 x 60 48 us against 60, 80 x 250 151 against 104).
+constexpr int solo_tokens(bool f32) { return f32 ? 64 : 256; }
 // Largest part that is taken for one part of one sequence per group, when equal
 // ranges would have `even` blocks: ranges cost a second item and its join.
 __host__ __device__ constexpr int64_t most_of(int64_t even) { return even + even / 5 + 16; }
@@ -91,6 +98,7 @@ struct Split {
   int share;         // blocks of a range
   int groups;        // groups of CTAs
   int aligned;       // one part of one sequence per group
+  int solo;          // whole sequences of one head, each by a warp of its own
 };
 
 // Attended tokens [lo, n) of a sequence whose length is given as n; lengths outside the table are cut.
@@ -133,6 +141,27 @@ __device__ __forceinline__ bool fixed_item(const Split& sp, Item* it, int grp, i
     const int j = j0 + part * kMinShare, jend = min(j + kMinShare, j0 + nb);
     *it = Item{b, h, s.lo, s.n, j, jend, grp - part, (nb + kMinShare - 1) / kMinShare, 0, jend - j, 0};
   }
+  __syncwarp();
+  return true;
+}
+
+// The warp's first or next item where warps take one sequence and head each (pos: which).
+template <int KB>
+__device__ __noinline__ bool solo_item(const Split* spp, Item* it, bool start) {
+  const Split& sp = *spp;
+  const int warps = gridDim.x * NW, units = sp.batch * sp.Hkv;
+  int u = start ? static_cast<int>(blockIdx.x) * NW + static_cast<int>(threadIdx.x) / 32 : static_cast<int>(it->pos) + warps;
+  int b = 0, nb = 0;
+  for (;; u += warps) {
+    if (u >= units) return false;
+    b = u / sp.Hkv;
+    nb = blocks_of<KB>(sp, b);
+    if (nb > 0) break;
+  }
+  const Span s = span_of(sp, sp.lens[b]);
+  const int j0 = s.lo / KB;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) *it = Item{b, u - b * sp.Hkv, s.lo, s.n, j0, j0 + nb, 0, 1, 0, nb, u};
   __syncwarp();
   return true;
 }
@@ -193,7 +222,7 @@ __device__ __noinline__ bool next_item(const Split* spp, Item* it, int nb0, bool
     const int j0 = s.lo / KB, nb = (s.n + KB - 1) / KB - j0;
     Item x;
     x.b = b; x.h = h; x.lo = s.lo; x.n = s.n; x.pos = pos;
-    if (sp.aligned) {                // part `skip`
+    if (sp.aligned) {         // part `skip`
       x.j = j0 + skip * sp.share;
       x.jend = min(x.j + sp.share, j0 + nb);
       x.left = x.jend - x.j;
@@ -757,16 +786,22 @@ struct FmaPieces {
   }
 };
 
-template <typename C>
-__global__ void __launch_bounds__(NW * 32, C::Geometry::CTAS)
-attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendArgs a, const AttendScratch sc) {
+struct AttendShared {
+  Split split[NW];
+  Item items[NW][2], open[2];
+  int last[2];
+};
+
+// The kernel after the split.  SOLO: warps take whole sequences and heads, and no two warps meet.
+template <typename C, bool SOLO>
+__device__ __forceinline__ void attend_items(const CUtensorMap& map, const AttendArgs& a, const AttendScratch& sc,
+                                             AttendShared& sh, int nb0, Span span0, uint8_t* smem) {
   using G_ = typename C::Geometry;
   using T = typename C::Elements;
   constexpr int D = C::kD, GP = C::kGP, KB = G_::KB, NSUB = G_::NSUB, NST = G_::NST;
   constexpr bool E4M3 = G_::SCALE > 0;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Split* const spp = &sh.split[warp];
   uint8_t* ring = smem + warp * NST * G_::STAGE;
   uint8_t* sring = smem + NW * NST * G_::STAGE + warp * NST * G_::SCALE;
   float* macc = reinterpret_cast<float*>(smem + NW * NST * (G_::STAGE + G_::SCALE));   // [NW][GP][D]
@@ -774,92 +809,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   uint64_t* bars = reinterpret_cast<uint64_t*>(mml + NW * GP * 4) + warp * NST;
   int32_t* live = reinterpret_cast<int32_t*>(reinterpret_cast<uint64_t*>(mml + NW * GP * 4) + NW * NST) + warp * NST;
   float* wbuf = reinterpret_cast<float*>(smem + G_::SMEM - 1024 - 256 - G_::WEIGHTS) + warp * (G_::WEIGHTS / (4 * NW));
-  __shared__ int last_[2];
-  __shared__ Item items[NW][2], open_[2];
-  __shared__ Split split_[NW];
-
-  if (lane == 0) {
-    if (!G_::F32) asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map)) : "memory");
-    for (int s = 0; s < NST; ++s) mbar_init(&bars[s], 1);
-    mbar_fence_init();
-  }
-  __syncwarp();
-
-  wait_for_prior_kernel();
-  // ---- the split ----
+  auto& items = sh.items;
   const int Hkv = a.pg.Hkv, G = a.G, n_cta = gridDim.x;
-  Split sp;
-  sp.lens = a.lens;
-  sp.batch = a.batch; sp.Hkv = Hkv; sp.window = a.window; sp.fixed = a.fixed;
-  sp.cap = static_cast<int>(min(static_cast<int64_t>(a.width) << a.pg.page_shift, static_cast<int64_t>(1 << 30)));
-  sp.groups = max(1, n_cta / Hkv);
-  sp.total = 0; sp.share = kMinShare; sp.aligned = 0;
-  int nb0 = 0;             // blocks of sequence `lane`
-  Span span0{0, 0};        // and its tokens
-  if (a.fixed > 0) {
-    if (warp == 0 && lane == 0 && blockIdx.x < a.batch) {
-      const int given = a.lens[blockIdx.x];
-      if (given != span_of(sp, given).n) set_error(a.pg.err, DEVERR_BAD_INDEX);
-    }
-  } else {
-    int64_t total = 0;
-    int longest = 0, seqs = 0;
-    bool bad_len = false;
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      const int b = b0 + lane;
-      int nb = 0;
-      Span s{0, 0};
-      if (b < a.batch) {
-        const int given = a.lens[b];
-        s = span_of(sp, given);
-        nb = (s.n + KB - 1) / KB - s.lo / KB;
-        bad_len |= given != s.n;
-      }
-      if (b0 == 0) {
-        nb0 = nb;
-        span0 = s;
-      }
-      total += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(nb));     // 32 sequences of at most 2^26 blocks
-      longest = max(longest, __reduce_max_sync(0xffffffffu, nb));
-      seqs += __popc(__ballot_sync(0xffffffffu, nb > 0));
-    }
-    if (bad_len && blockIdx.x == 0 && warp == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
-    sp.total = total;
-    const int64_t even = quotient(total + sp.groups - 1, sp.groups);
-    sp.share = static_cast<int>(min(max(even, static_cast<int64_t>(kMinShare)), static_cast<int64_t>(1 << 30)));
-    if (seqs > 0 && seqs <= sp.groups) {
-      // the smallest largest part with which there are no more parts than groups
-      auto fits = [&](int s) {
-        int items = 0;
-        for (int b0 = 0; b0 < a.batch; b0 += 32) {
-          int nb = 0;
-          if (b0 + lane < a.batch) nb = b0 == 0 ? nb0 : blocks_of<KB>(sp, b0 + lane);
-          const int np = static_cast<int>(static_cast<uint32_t>(nb + s - 1) / static_cast<uint32_t>(s));
-          items += __reduce_add_sync(0xffffffffu, min(np, sp.groups + 1));
-        }
-        return items <= sp.groups;
-      };
-      const int per = sp.groups / seqs;
-      int lo = sp.share, hi = (longest + per - 1) / per;     // hi fits: no sequence has more than `per` parts
-      if (hi <= lo || fits(lo)) {
-        hi = lo;
-      } else {
-        while (hi - lo > 1 + lo / 32) {
-          const int mid = lo + (hi - lo) / 2;
-          if (fits(mid)) hi = mid;
-          else lo = mid;
-        }
-      }
-      if (hi <= most_of(sp.share)) {
-        sp.aligned = 1;
-        sp.share = hi;
-      }
-    }
-  }
-  if (lane == 0) split_[warp] = sp;
-  __syncwarp();
-  const Split* const spp = &split_[warp];
-
   // sequences without a token
   auto zeros = [&]() {
     for (int b = blockIdx.x; b < a.batch; b += n_cta) {
@@ -873,12 +824,14 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
 
   // ---- items: the one in hand, and the producer's, NST blocks ahead ----
   bool some;
-  if (a.fixed > 0) {
-    some = n_cta >= Hkv && fixed_item<KB>(sp, &items[warp][0], blockIdx.x / Hkv, blockIdx.x % Hkv);
-  } else if (sp.aligned && a.batch <= 32 && n_cta >= Hkv) {
+  if constexpr (SOLO) {
+    some = solo_item<KB>(spp, &items[warp][0], true);
+  } else if (a.fixed > 0) {
+    some = n_cta >= Hkv && fixed_item<KB>(*spp, &items[warp][0], blockIdx.x / Hkv, blockIdx.x % Hkv);
+  } else if (spp->aligned && a.batch <= 32 && n_cta >= Hkv) {
     // what next_item does, from what the lanes already have
     const int grp = blockIdx.x / Hkv;
-    const int own = static_cast<int>(static_cast<uint32_t>(nb0 + sp.share - 1) / static_cast<uint32_t>(sp.share));
+    const int own = static_cast<int>(static_cast<uint32_t>(nb0 + spp->share - 1) / static_cast<uint32_t>(spp->share));
     int sum = own;
     if (a.batch > 1) {
 #pragma unroll
@@ -888,16 +841,16 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
       }
     }
     const unsigned past = __ballot_sync(0xffffffffu, sum > grp);
-    some = past != 0 && grp < sp.groups;
+    some = past != 0 && grp < spp->groups;
     if (some && lane == __ffs(past) - 1) {
-      const int part = grp - (sum - own), j0 = span0.lo / KB, j = j0 + part * sp.share, jend = min(j + sp.share, j0 + nb0);
+      const int part = grp - (sum - own), j0 = span0.lo / KB, j = j0 + part * spp->share, jend = min(j + spp->share, j0 + nb0);
       items[warp][0] = Item{lane, static_cast<int>(blockIdx.x) - grp * Hkv, span0.lo, span0.n, j, jend, grp - part, own, 0, jend - j, 0};
     }
     __syncwarp();
   } else {
     some = next_item<KB>(spp, &items[warp][0], nb0, true);
   }
-  if (!some) {            // the whole CTA
+  if (!some) {            // the whole CTA, or (SOLO) this warp alone
     zeros();
     return;
   }
@@ -906,14 +859,19 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   const Item& w = items[warp][0];
   Item& p = items[warp][1];
   // first own block of an item: blocks go to the warps in turn
-  auto first_own = [&](int j) { return j + ((warp - j) & (NW - 1)); };
+  constexpr int kStride = SOLO ? 1 : NW;
+  auto first_own = [&](int j) { return SOLO ? j : j + ((warp - j) & (NW - 1)); };
+  auto next = [&](Item* it) {
+    if constexpr (SOLO) return solo_item<KB>(spp, it, false);
+    else return next_item<KB>(spp, it, nb0, false);
+  };
   bool dead = false;     // a wait ran out: nothing more is copied or computed
   bool p_more = true;
   int pj = first_own(p.j), p_end = p.jend, seq_p = 0, page_next = -1;
   bool page_want = false;
   auto settle = [&]() {  // moves p to an item that has a block for this warp
     while (p_more && pj >= p_end) {
-      p_more = next_item<KB>(spp, &p, nb0, false);
+      p_more = next(&p);
       pj = first_own(p.j);
       p_end = p.jend;
     }
@@ -951,7 +909,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
       }
     }
     ++seq_p;
-    pj += NW;
+    pj += kStride;
     settle();
     load_page();
   };
@@ -969,7 +927,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
     bool any = false;
     const int lo = w.lo, n = w.n, jend = w.jend;
 
-    for (int j = first_own(w.j); j < jend; j += NW) {
+    for (int j = first_own(w.j); j < jend; j += kStride) {
       const int st = seq_c % NST;
       if (!dead && !mbar_wait(&bars[st], (seq_c / NST) & 1)) {
         if (lane == 0) set_error(a.pg.err, DEVERR_TIMEOUT);
@@ -995,15 +953,17 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
 
     // ---- join the warps ----
     c.close(macc, mml, warp, any);
-    __syncthreads();
-    const bool complete = w.parts == 1;
+    if constexpr (SOLO) __syncwarp();
+    else __syncthreads();
+    const bool complete = SOLO || w.parts == 1;
     const int64_t slot = complete ? 0 : slot_of(w, static_cast<int>(blockIdx.x) / Hkv - w.first, Hkv);
     const int64_t orow = static_cast<int64_t>(w.b) * a.Hq + static_cast<int64_t>(w.h) * G;
-    for (int i = threadIdx.x; i < G * (D / 4); i += NW * 32) {
+    for (int i = SOLO ? lane : threadIdx.x; i < G * (D / 4); i += SOLO ? 32 : NW * 32) {
       const int q = i / (D / 4), e = (i % (D / 4)) * 4;
       float M = -INFINITY, seen = 0.f;
 #pragma unroll
       for (int x = 0; x < NW; ++x) {
+        if (SOLO && x != warp) continue;
         M = fmaxf(M, mml[(x * GP + q) * 4]);
         seen += mml[(x * GP + q) * 4 + 2];
       }
@@ -1012,6 +972,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < NW; ++x) {
+        if (SOLO && x != warp) continue;
         if (mml[(x * GP + q) * 4 + 2] == 0.f) continue;
         const float c = ex2(mml[(x * GP + q) * 4] - mu);
         const float4 v = *reinterpret_cast<const float4*>(&macc[(x * GP + q) * D + e]);
@@ -1027,26 +988,27 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
       }
     }
     if (!complete) {
-      if (threadIdx.x == 0) open_[n_open] = w;
+      if (threadIdx.x == 0) sh.open[n_open] = w;
       ++n_open;
     }
-    __syncthreads();     // the join's buffers are free again
-    more = next_item<KB>(spp, &items[warp][0], nb0, false);
+    if constexpr (SOLO) __syncwarp();      // the join's buffers are free again
+    else __syncthreads();
+    more = next(&items[warp][0]);
   }
   // ---- sequences that lie in other ranges too (the range's first and last): join them if all parts are there ----
   // Left for the end, since each step waits for the one before at the far side of L2, 2 us and more while the
   // GPU reads at full speed.
-  if (n_open > 0) {
+  if (!SOLO && n_open > 0) {
     __threadfence();
     __syncthreads();
     if (threadIdx.x < n_open) {
-      const Item& x = open_[threadIdx.x];
-      last_[threadIdx.x] = atomicAdd(&sc.ticket[static_cast<int64_t>(x.b) * Hkv + x.h], 1) == x.parts - 1;
+      const Item& x = sh.open[threadIdx.x];
+      sh.last[threadIdx.x] = atomicAdd(&sc.ticket[static_cast<int64_t>(x.b) * Hkv + x.h], 1) == x.parts - 1;
     }
     __syncthreads();
     for (int i_open = 0; i_open < n_open; ++i_open) {
-      if (!last_[i_open]) continue;
-      const Item& x = open_[i_open];
+      if (!sh.last[i_open]) continue;
+      const Item& x = sh.open[i_open];
       const int64_t orow = static_cast<int64_t>(x.b) * a.Hq + static_cast<int64_t>(x.h) * G;
       __threadfence();
       if (threadIdx.x == 0) sc.ticket[static_cast<int64_t>(x.b) * Hkv + x.h] = 0;
@@ -1090,6 +1052,102 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   // copies that a dead warp leaves in flight: wait for them (bounded) before its shared memory goes
   if (dead)
     for (; seq_c < seq_p; ++seq_c) mbar_wait(&bars[seq_c % NST], (seq_c / NST) & 1);
+}
+
+template <typename C>
+__global__ void __launch_bounds__(NW * 32, C::Geometry::CTAS)
+attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendArgs a, const AttendScratch sc) {
+  using G_ = typename C::Geometry;
+  constexpr int D = C::kD, GP = C::kGP, KB = G_::KB, NST = G_::NST;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NW * NST * (G_::STAGE + G_::SCALE) + NW * GP * (D + 4) * 4) + warp * NST;
+  __shared__ AttendShared sh;
+  if (lane == 0) {
+    if (!G_::F32) asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map)) : "memory");
+    for (int s = 0; s < NST; ++s) mbar_init(&bars[s], 1);
+    mbar_fence_init();
+  }
+  __syncwarp();
+
+  wait_for_prior_kernel();
+  // ---- the split ----
+  const int Hkv = a.pg.Hkv, n_cta = gridDim.x;
+  Split sp;
+  sp.lens = a.lens;
+  sp.batch = a.batch; sp.Hkv = Hkv; sp.window = a.window; sp.fixed = a.fixed;
+  sp.cap = static_cast<int>(min(static_cast<int64_t>(a.width) << a.pg.page_shift, static_cast<int64_t>(1 << 30)));
+  sp.groups = max(1, n_cta / Hkv);
+  sp.total = 0; sp.share = kMinShare; sp.aligned = 0; sp.solo = 0;
+  int nb0 = 0;             // blocks of sequence `lane`
+  Span span0{0, 0};        // and its tokens
+  if (a.fixed > 0) {
+    if (warp == 0 && lane == 0 && blockIdx.x < a.batch) {
+      const int given = a.lens[blockIdx.x];
+      if (given != span_of(sp, given).n) set_error(a.pg.err, DEVERR_BAD_INDEX);
+    }
+  } else {
+    int64_t total = 0;
+    int longest = 0, seqs = 0;
+    bool bad_len = false;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const int b = b0 + lane;
+      int nb = 0;
+      Span s{0, 0};
+      if (b < a.batch) {
+        const int given = a.lens[b];
+        s = span_of(sp, given);
+        nb = (s.n + KB - 1) / KB - s.lo / KB;
+        bad_len |= given != s.n;
+      }
+      if (b0 == 0) {
+        nb0 = nb;
+        span0 = s;
+      }
+      total += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(nb));     // 32 sequences of at most 2^26 blocks
+      longest = max(longest, __reduce_max_sync(0xffffffffu, nb));
+      seqs += __popc(__ballot_sync(0xffffffffu, nb > 0));
+    }
+    if (bad_len && blockIdx.x == 0 && warp == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
+    sp.total = total;
+    const int64_t even = quotient(total + sp.groups - 1, sp.groups);
+    sp.share = static_cast<int>(min(max(even, static_cast<int64_t>(kMinShare)), static_cast<int64_t>(1 << 30)));
+    if (longest * KB <= solo_tokens(G_::F32) && seqs > sp.groups) {
+      sp.solo = 1;
+    } else if (seqs > 0 && seqs <= sp.groups) {
+      // the smallest largest part with which there are no more parts than groups
+      auto fits = [&](int s) {
+        int items = 0;
+        for (int b0 = 0; b0 < a.batch; b0 += 32) {
+          int nb = 0;
+          if (b0 + lane < a.batch) nb = b0 == 0 ? nb0 : blocks_of<KB>(sp, b0 + lane);
+          const int np = static_cast<int>(static_cast<uint32_t>(nb + s - 1) / static_cast<uint32_t>(s));
+          items += __reduce_add_sync(0xffffffffu, min(np, sp.groups + 1));
+        }
+        return items <= sp.groups;
+      };
+      const int per = sp.groups / seqs;
+      int lo = sp.share, hi = (longest + per - 1) / per;     // hi fits: no sequence has more than `per` parts
+      if (hi <= lo || fits(lo)) {
+        hi = lo;
+      } else {
+        while (hi - lo > 1 + lo / 32) {
+          const int mid = lo + (hi - lo) / 2;
+          if (fits(mid)) hi = mid;
+          else lo = mid;
+        }
+      }
+      if (hi <= most_of(sp.share)) {
+        sp.aligned = 1;
+        sp.share = hi;
+      }
+    }
+  }
+  if (lane == 0) sh.split[warp] = sp;
+  __syncwarp();
+  if (sp.solo) attend_items<C, true>(map, a, sc, sh, nb0, span0, smem);
+  else attend_items<C, false>(map, a, sc, sh, nb0, span0, smem);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {

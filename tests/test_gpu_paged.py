@@ -516,6 +516,30 @@ def test_attend_does_not_depend_on_the_table_s_width(dtype, cache, d, g, hkv, pa
                 check_attend(out[b], lse[b], q[b], x[:, :, 0], x[:, :, 1], dtype, window=window)
 
 
+@pytest.mark.parametrize("dtype,cache,d,g,hkv,page", [("bf16", "native", 128, 4, 4, 16), ("bf16", "native", 64, 8, 6, 32),
+                                                      ("bf16", "e4m3", 128, 2, 8, 16), ("bf16", "e4m3", 64, 16, 5, 64),
+                                                      ("f32", "native", 128, 3, 4, 16), ("f32", "native", 64, 9, 4, 16)])
+@pytest.mark.parametrize("most,window", [(17, 0), (60, 0), (90, 33), (257, 0)])
+def test_attend_many_short_sequences(dtype, cache, d, g, hkv, page, most, window):
+    """More short sequences than blocks of the GPU: each head of each goes to a warp of its own."""
+    lens = [int(x) for x in np.random.default_rng(most).integers(0, most, size=250)]
+    b, n = len(lens), max(lens)
+    table, n_pages = tables(lens, page, 3)
+    wide = np.full((b, 600), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    k, v = rows((b, n, hkv, d), dtype, 4), rows((b, n, hkv, d), dtype, 5)
+    c = cache_of(g * hkv, hkv, d, page, n_pages, dtype, cache, max_batch=256)
+    c.append(0, k, v, ints(slots_of(table, lens, page, n)))
+    q = rows((b, g * hkv, d), dtype, 6)
+    out, lse = torch.full_like(q, 7), torch.full(q.shape[:2], 7.0, device="cuda")
+    for _ in range(2):
+        c.attend(0, q, ints(wide), ints(lens), out, lse, window=window)
+    for i in range(0, b, 9):
+        x = held_rows(c, 0, table, lens[i], page, i)
+        check_attend(out[i], lse[i], q[i], x[:, :, 0], x[:, :, 1], dtype, window=window)
+    assert torch.isfinite(out).all() and c.get_error() == (kp.KVPOP_OK, 0)
+
+
 def test_offsets_past_32_bits():
     """The last pages of a pool of more than 2^31 elements and 2^32 bytes."""
     page, hkv, d = 256, 8, 128
