@@ -601,7 +601,7 @@ class KVPopPagedCache:
     def attend(self, layer: int, q, page_table, lens, out, lse=None, scale=0.0, softcap=0.0, window=0,
                stream=None) -> None:
         """Attention of one new token per sequence: q, out [batch][q heads]
-        [head_dim]; lse fp32 [batch][q heads] or None.  scale 0: 1 / sqrt(head_dim);
+        [head_dim], out may be q; lse fp32 [batch][q heads] or None.  scale 0: 1 / sqrt(head_dim);
         softcap > 0: scores become softcap * tanh(score / softcap); window > 0:
         the last `window` tokens alone are attended."""
         _check(_binding.attend(self._attend, self._args, layer, q, page_table, lens, out, lse, scale, softcap, window,

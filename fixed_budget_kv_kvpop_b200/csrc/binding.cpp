@@ -7,6 +7,8 @@
 // ABI call that it makes, so that any build of the library can stand behind it.
 #include <Python.h>
 
+#include <cmath>
+
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -294,8 +296,9 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return nullptr;
   const double scale = PyFloat_AsDouble(a[8]), cap = PyFloat_AsDouble(a[9]);
   if (PyErr_Occurred()) return nullptr;
-  o.scale = static_cast<float>(scale);
-  o.softcap = static_cast<float>(cap);
+  // 0 is the default: what only rounds to 0 is not taken for it
+  o.scale = scale != 0 && static_cast<float>(scale) == 0.f ? NAN : static_cast<float>(scale);
+  o.softcap = cap != 0 && static_cast<float>(cap) == 0.f ? NAN : static_cast<float>(cap);
   return call([&] {
     return fn(c.h, layer, q, table, width, width, lens, static_cast<int32_t>(b), &o, out, static_cast<float*>(lse), st);
   });

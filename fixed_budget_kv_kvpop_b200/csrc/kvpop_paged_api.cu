@@ -149,6 +149,9 @@ PagedLayer paged_layer(const kvpop_paged_handle* h, int layer) {
   return p;
 }
 
+// 0 (the default) or a factor whose products and reciprocals with the kernel's constants stay normal numbers.
+bool factor_ok(float x) { return x == 0.f || (x >= 0x1p-100f && x <= 0x1p100f); }
+
 bool bad_layer(const kvpop_paged_handle* h, int32_t layer) { return !h || layer < 0 || layer >= h->cfg.n_layers; }
 
 // Page table and lengths of `batch` sequences.
@@ -310,8 +313,7 @@ int kvpop_paged_attend(kvpop_paged_handle* h, int32_t layer, const void* q, cons
   const kvpop_paged_config& c = h->cfg;
   if (batch > c.max_batch) return KVPOP_ERR_BAD_SHAPE;
   const kvpop_attend_options o = options ? *options : kvpop_attend_options{0.f, 0.f, 0};
-  if (!(o.scale >= 0.f) || !std::isfinite(o.scale) || !(o.softcap >= 0.f) || !std::isfinite(o.softcap) || o.window < 0)
-    return KVPOP_ERR_INVALID_ARG;
+  if (!factor_ok(o.scale) || !factor_ok(o.softcap) || o.window < 0) return KVPOP_ERR_INVALID_ARG;
   if (batch == 0) return KVPOP_OK;
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return KVPOP_ERR_INVALID_ARG;
   if (!tables_ok(page_table, table_stride, table_width, lens, batch)) return KVPOP_ERR_INVALID_ARG;

@@ -418,7 +418,7 @@ typedef struct kvpop_rows {
 typedef struct kvpop_rope {
   const float* q_weight;    /* fp32 [head_dim] or NULL, 16-byte aligned */
   const float* k_weight;    /* fp32 [head_dim] or NULL, 16-byte aligned */
-  const double* inv_freq;   /* fp64 [rot_dim / 2] */
+  const double* inv_freq;   /* fp64 [rot_dim / 2], finite */
   float eps;                /* >= 0 */
   float rot_scale;
   int32_t rot_dim;          /* multiple of 8, 0 <= rot_dim <= head_dim; 0 = no rotation */
@@ -514,7 +514,8 @@ int kvpop_paged_gather(kvpop_paged_handle* h, int32_t layer, const int32_t* page
                        int32_t table_width, const int32_t* lens, int32_t batch, int32_t n_tokens,
                        const kvpop_rows* k_out, const kvpop_rows* v_out, void* stream);
 
-/* Options of kvpop_paged_attend; a null pointer means all zero. */
+/* Options of kvpop_paged_attend; a null pointer means all zero.  scale and
+ * softcap, where not 0, lie in [2^-100, 2^100]. */
 typedef struct kvpop_attend_options {
   float scale;      /* > 0, or 0 = 1 / sqrt(head_dim) */
   float softcap;    /* > 0: scores become softcap * tanh(score / softcap); 0 = none */
@@ -527,7 +528,7 @@ typedef struct kvpop_attend_options {
  * one launch; the work of all sequences is split evenly over the GPU along
  * the cache's length and joined in a fixed order, so equal calls give equal
  * bits.  q, out: device [batch][n_q_heads][head_dim] in dtype, 16-byte
- * aligned; lse: device fp32 [batch][n_q_heads] receiving log sum_j e^(s_j),
+ * aligned, and out may be q; lse: device fp32 [batch][n_q_heads] receiving log sum_j e^(s_j),
  * or NULL.  page_table, lens as kvpop_paged_gather; 0 <= batch <= max_batch,
  * table_width * page_size <= 2^30.
  * A sequence with no token gets out = 0, lse = -inf.  Infinities and NaN in

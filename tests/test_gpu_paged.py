@@ -126,6 +126,23 @@ def test_heads(dtype, d, hq, hkv, rot, inter, norm, scale, b, n):
             assert (err <= bound).all(), float((err / bound).max())
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_heads_at_negative_positions(inter):
+    """Angles of positions below zero, down to the lowest."""
+    x = rows((1, 6, 3, 64), "f32", 8)
+    freq = 1e5 ** (-np.arange(0, 64, 2) / 64)
+    # More than a turn per position; backwards.  At 2^31 the angle 9.5 pos is off by 2^31 ulp(1.5) / 2 = 2^-22 turns
+    # (1.5e-6) here and by ulp(2e10) / 2 = 1.9e-6 in the formula: with the 4 U of the rest below the 128 U of the bound.
+    freq[3], freq[5] = 9.5, -0.25
+    rope = kp.make_rope(torch.from_numpy(freq).cuda(), interleaved=inter, eps=1e-6)
+    pos = np.array([[-1, -2, -4097, 5, -2 ** 31, -2 ** 31 + 1]], np.int32)
+    qo, ko = torch.empty_like(x[:, :, :2]), torch.empty_like(x[:, :, 2:])
+    kp.qk_norm_rope(rope, x[:, :, :2], x[:, :, 2:], ints(pos), qo, ko)
+    for got, src in ((qo, x[:, :, :2]), (ko, x[:, :, 2:])):
+        want, bound = heads_bound(f64(src[0]), None, 1e-6, pos[0], freq, 1.0, inter, "f32")
+        assert (np.abs(f64(got[0]) - want) <= bound).all()
+
+
 def test_heads_in_place_and_broadcast_input():
     """q_out = q, k_out = k; and one key head expanded over four."""
     x = rows((2, 9, 6, 64), "bf16", 1)
@@ -353,11 +370,11 @@ def check_attend(out, lse, q, k, v, dtype, scale=None, softcap=0.0, window=0):
         assert (np.abs(got[ok] - wl[ok]) <= (ls + 4 * U * np.abs(wl) + 4 * U)[ok]).all()
 
 
-def filled(lens, hq, hkv, d, page, dtype, cache, seed=0):
+def filled(lens, hq, hkv, d, page, dtype, cache, seed=0, **kw):
     b, n = len(lens), max(max(lens), 1)
     table, n_pages = tables(lens, page, seed)
     k, v = rows((b, n, hkv, d), dtype, seed + 1), rows((b, n, hkv, d), dtype, seed + 2)
-    c = cache_of(hq, hkv, d, page, n_pages, dtype, cache)
+    c = cache_of(hq, hkv, d, page, n_pages, dtype, cache, **kw)
     c.append(0, k, v, ints(slots_of(table, lens, page, n)))
     return c, table, rows((b, hq, d), dtype, seed + 3)
 
@@ -382,6 +399,19 @@ def test_attend(dtype, cache, d, g, hkv, page, lens):
     for b, n in enumerate(lens):
         x = held_rows(c, 0, table, n, page, b)
         check_attend(out[b], lse[b], q[b], x[:, :, 0], x[:, :, 1], dtype)
+
+
+@pytest.mark.parametrize("dtype,cache,d,g,hkv,page", [SHAPES[0], SHAPES[5], SHAPES[9]])
+@pytest.mark.parametrize("lens,width", [([40, 0, 3], 0), ([2900, 17], 0), ([2900, 700, 64], 4000), ([33] * 300, 0), ([900, 20] * 120, 0)])
+def test_attend_in_place(dtype, cache, d, g, hkv, page, lens, width):
+    """out = q, for each way of splitting the work: the bits of a call with a separate out."""
+    c, table, q = filled(lens, g * hkv, hkv, d, page, dtype, cache, seed=12, max_batch=512)
+    wide = np.zeros((len(lens), max(width, table.shape[1])), np.int32)
+    wide[:, :table.shape[1]] = table
+    want = torch.empty_like(q)
+    c.attend(0, q, ints(wide), ints(lens), want)
+    c.attend(0, q, ints(wide), ints(lens), q)
+    assert torch.equal(q, want) and c.get_error() == (kp.KVPOP_OK, 0)
 
 
 @pytest.mark.parametrize("dtype,cache,d,g,hkv,page", [SHAPES[0], SHAPES[5], SHAPES[8], SHAPES[6], SHAPES[3]])
@@ -669,7 +699,8 @@ def test_refusals_on_the_gpu():
     with pytest.raises(kp.KVPopError) as e:
         c.attend(0, q, t, n, torch.empty_like(q))                    # three sequences, max_batch two
     assert e.value.status == kp.KVPOP_ERR_BAD_SHAPE
-    for kw in (dict(scale=-1.0), dict(softcap=-1.0), dict(window=-1), dict(scale=math.nan), dict(softcap=math.inf)):
+    for kw in (dict(scale=-1.0), dict(softcap=-1.0), dict(window=-1), dict(scale=math.nan), dict(softcap=math.inf),
+               dict(scale=1e-40), dict(softcap=1e-40), dict(scale=3e38), dict(softcap=3e38), dict(scale=1e-60), dict(softcap=1e-60)):
         with pytest.raises(kp.KVPopError) as e:
             c.attend(0, q[:2], t[:2], n[:2], torch.empty_like(q[:2]), **kw)
         assert e.value.status == kp.KVPOP_ERR_INVALID_ARG
