@@ -675,6 +675,96 @@ def test_two_caches_on_two_streams():
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_two_caches_fork_and_join(captured):
+    """A step of two layers in two caches whose writes fork to a second stream and join again, captured and eager, ten times."""
+    b, hq, hkv, d, page = 5, 8, 2, 128, 16
+    freq = torch.from_numpy(1e4 ** (-np.arange(0, d, 2) / d)).cuda()
+    rope = kp.make_rope(freq, q_weight=torch.ones(d, device="cuda"), k_weight=torch.ones(d, device="cuda"))
+    start = np.array([0, 13, 500, 31, 64])
+    table, n_pages = tables([600] * b, page, 1)
+    tab, steps = ints(table), 10
+    xs = rows((steps, b, 1, hq + 2 * hkv, d), "bf16", 1)
+
+    def caches():
+        cs = [cache_of(hq, hkv, d, page, n_pages, cache=f) for f in ("native", "e4m3")]
+        for c in cs:
+            k = rows((b, 500, hkv, d), "bf16", 2)
+            c.append(0, k, k, ints(slots_of(table, list(start), page, 500)))
+        return cs
+
+    side = torch.cuda.Stream()
+
+    def step(cs, x, pos, slot, lens, qo, out, fork):
+        here = torch.cuda.current_stream()
+        if fork:
+            side.wait_stream(here)
+        cs[0].append_qkv(0, rope, x[:, :, :hq], x[:, :, hq:hq + hkv], x[:, :, hq + hkv:], pos, slot, qo[0])
+        with torch.cuda.stream(side if fork else here):
+            cs[1].append_qkv(0, rope, x[:, :, :hq], x[:, :, hq:hq + hkv], x[:, :, hq + hkv:], pos, slot, qo[1])
+            cs[1].attend(0, qo[1][:, 0], tab, lens, out[1])
+        cs[0].attend(0, qo[0][:, 0], tab, lens, out[0])
+        if fork:
+            here.wait_stream(side)
+        kp.qk_norm_rope(rope, out[0].unsqueeze(1), out[1][:, :hkv].unsqueeze(1), pos, out[2].unsqueeze(1), out[3][:, :hkv].unsqueeze(1))
+
+    one, two = caches(), caches()
+    x, pos, slot, lens = xs[0].clone(), ints(np.zeros((b, 1))), ints(np.zeros((b, 1))), ints(np.zeros(b))
+    bufs = [([torch.zeros(b, 1, hq, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)],
+             [torch.zeros(b, hq, d, dtype=torch.bfloat16, device="cuda") for _ in range(4)]) for _ in range(2)]
+    main = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=main):
+            step(one, x, pos, slot, lens, *bufs[0], True)
+    for i in range(steps):
+        at = start + i
+        x.copy_(xs[i])
+        pos.copy_(ints(at[:, None]))
+        slot.copy_(ints((table[np.arange(b), at // page] * page + at % page)[:, None]))
+        lens.copy_(ints(at + 1))
+        torch.cuda.synchronize()
+        if captured:
+            g.replay()
+        else:
+            with torch.cuda.stream(main):
+                step(one, x, pos, slot, lens, *bufs[0], True)
+        torch.cuda.synchronize()
+        step(two, x, pos, slot, lens, *bufs[1], False)
+        torch.cuda.synchronize()
+        for p, q in zip(bufs[0][1], bufs[1][1]):
+            assert torch.equal(p, q)
+    for c in one + two:
+        assert c.get_error() == (kp.KVPOP_OK, 0)
+
+
+def test_calls_from_two_threads():
+    """Two host threads, each with its own stream and cache, at once."""
+    from concurrent.futures import ThreadPoolExecutor
+    lens = [300, 17, 0, 64]
+    made = [filled(lens, 8, 2, 128, 16, "bf16", f, seed=3) for f in ("native", "e4m3")]
+    want = []
+    for c, table, q in made:
+        out = torch.empty_like(q)
+        c.attend(0, q, ints(table), ints(lens), out)
+        want.append(out)
+    torch.cuda.synchronize()
+
+    def work(i):
+        c, table, q = made[i]
+        s, t, n = torch.cuda.Stream(), ints(table), ints(lens)
+        outs = [torch.empty_like(q) for _ in range(200)]
+        torch.cuda.synchronize()
+        for o in outs:
+            c.attend(0, q, t, n, o, stream=s)
+        s.synchronize()
+        return all(torch.equal(o, want[i]) for o in outs)
+
+    with ThreadPoolExecutor(2) as pool:
+        assert all(pool.map(work, range(2)))
+
+
 def test_refusals_on_the_gpu():
     c = cache_of(4, 2, 64, 16, 4, max_batch=2)
     k = rows((1, 3, 2, 64), "bf16", 1)
