@@ -126,6 +126,31 @@ def test_heads(dtype, d, hq, hkv, rot, inter, norm, scale, b, n):
             assert (err <= bound).all(), float((err / bound).max())
 
 
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("dtype,d,rot,inter", [("bf16", 128, 64, False), ("bf16", 128, 40, True), ("f32", 64, 24, False),
+                                               ("f32", 64, 0, False), ("bf16", 64, 8, False), ("f32", 128, 120, True)])
+def test_heads_nonfinite_elements_that_are_not_turned(dtype, d, rot, inter, norm):
+    """An infinity or a NaN behind rot_dim reaches no other element but through the row's norm."""
+    x = rows((1, 5, 4, d), dtype, 9)
+    for t, (e, bad) in enumerate([(rot, math.inf), (d - 1, -math.inf), (d // 2 + 1 if d // 2 >= rot else d - 3, math.nan), (d - 2, math.inf)]):
+        x[0, t, :, e] = bad
+    freq = 1e4 ** (-np.arange(0, rot, 2) / max(rot, 1))
+    w = 1 + 0.2 * np.random.default_rng(2).normal(size=d).astype(np.float32)
+    wt = torch.from_numpy(w).cuda()
+    rope = kp.make_rope(torch.from_numpy(freq).cuda(), interleaved=inter, **(dict(q_weight=wt, k_weight=wt) if norm else {}))
+    pos = np.array([[3, 1000, 77, 0, 9]], np.int32)
+    qo, ko = torch.empty_like(x[:, :, :3]), torch.empty_like(x[:, :, 3:])
+    kp.qk_norm_rope(rope, x[:, :, :3], x[:, :, 3:], ints(pos), qo, ko)
+    with np.errstate(invalid="ignore"):
+        for got, src in ((qo, x[:, :, :3]), (ko, x[:, :, 3:])):
+            want, bound = heads_bound(f64(src[0]), w if norm else None, 1e-6, pos[0], freq, 1.0, inter, dtype)
+            got = f64(got[0])
+            assert (np.isnan(got) == np.isnan(want)).all()
+            sure = np.isfinite(want)
+            assert (got[~sure & ~np.isnan(want)] == want[~sure & ~np.isnan(want)]).all()
+            assert (np.abs(got - want)[sure] <= bound[sure]).all()
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_heads_at_negative_positions(inter):
     """Angles of positions below zero, down to the lowest."""
