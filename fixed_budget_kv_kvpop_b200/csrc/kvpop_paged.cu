@@ -202,13 +202,14 @@ __device__ __forceinline__ void store_e4m3(uint8_t* row, const Places& at, const
 // the lane that asked for them reads, so that they need no registers and no
 // barrier.  ALL: every element is turned (telling them apart takes 16 selects
 // a pass: 8192 tokens of 40 heads 33.5 us without, 34.6 us with).
+constexpr int kHeadsDepth = 3;      // 4096 tokens of 40 heads: 3 18.4 us, 4 18.2, 6 18.6, 8 19.0; 8192: 33.1, 33.4, 33.4, 34.3; 32768: 112, 122, 123, 121
 template <typename T, int D, bool E4M3, int MODE, bool INTER, bool WIDE, bool ALL>
 __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constant__ HeadsArgs a, int q_passes, int kv_passes, int wpt_shift) {
   constexpr int LPR = D / 16;         // lanes per row
   constexpr int RPW = 32 / LPR;       // rows per warp and pass
   constexpr int kSlots = D / 64;      // pairs of a lane, at most
   constexpr int PASS = 32 * 16 * sizeof(T);      // bytes of a pass
-  constexpr int DEPTH = sizeof(T) == 2 ? 6 : 4;
+  constexpr int DEPTH = kHeadsDepth;
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % LPR, sub = lane / LPR;
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 2) heads_kernel(const __grid_constan
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 template <typename T, int D>
-constexpr int heads_smem() { return (kThreads / 32) * ((sizeof(T) == 2 ? 6 : 4) * 32 * 16 * static_cast<int>(sizeof(T)) + 4 * D * 4); }
+constexpr int heads_smem() { return (kThreads / 32) * (kHeadsDepth * 32 * 16 * static_cast<int>(sizeof(T)) + 4 * D * 4); }
 
 // Keys and values of new tokens into pages.  Bound by HBM.  A warp takes one
 // token's keys or values (blockIdx.y: which, and which `chunk` of their
