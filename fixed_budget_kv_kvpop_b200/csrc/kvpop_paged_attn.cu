@@ -81,6 +81,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Four e4m3 bytes -> bf16 pairs of bytes 0, 2 and of bytes 1, 3, exactly.
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t x, uint32_t& even, uint32_t& odd) {
+  const uint32_t lo = e4m3_to_f16(x), hi = e4m3_to_f16_high(x);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  even = __byte_perm(__float_as_uint(a.x), __float_as_uint(b.x), 0x7632);   // four significant bits: the upper halves are all
+  odd = __byte_perm(__float_as_uint(a.y), __float_as_uint(b.y), 0x7632);
+}
+
 // a / b for a >= 0, b > 0: in 32 bits where a allows, a fraction of the 64-bit division's time.
 __device__ __forceinline__ int64_t quotient(int64_t a, int b) {
   if ((a >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
@@ -295,10 +304,13 @@ __device__ __forceinline__ void write4(float* p, const float4& o, float L, bool 
 // heads fill rows 0..3 and again 4..7), and its accumulator fragment, as
 // weights, is the B fragment of O^T += V^T P^T.  Weights go in as two bf16
 // terms (16 bits): with up to four heads the repeated rows carry the low
-// terms, so they cost nothing, else a second instruction does.  8-bit rows are
-// widened to f16, exactly (queries then are f16 too, scaled by a power of two,
-// and weights are two f16 terms); a key's scale multiplies its score, a
-// value's scale its weight.
+// terms, so they cost nothing, else a second instruction does.  8-bit keys are
+// widened to f16, exactly (queries then are f16 too, scaled by a power of two),
+// 8-bit values to bf16: a key's scale multiplies its score, a value's scale
+// its weight, and only bf16 holds every weight times every scale to the same
+// 16 bits.  (Values and weights in f16 take fewer instructions, but need one
+// reference for all weights of a warp, 2^31 below which a token is lost:
+// 32 x 32768 took 257 us so, 267 us in bf16.)
 template <int D, bool E4M3, int GP>
 struct MmaPieces {
   using Geometry = Geo<__nv_bfloat16, D, E4M3, GP>;
@@ -312,11 +324,6 @@ struct MmaPieces {
   float qmul[R];
   float acc[R][KS][4];
   float m[R], l[R];
-  // 8 bits: weights are p * scale * vmul with vmul = 64 / vref, vref a power of
-  // two above half the largest value scale so far (2^-100 at least): at most
-  // 2^15, and a weight's two f16 terms are exact to 2^-25, 2^-31 of a weight
-  // of one with the largest scale
-  float vref, vmul;
   uint32_t kx[2], vx[4];      // this lane's offsets into a piece, for its loads of keys and of values
 
   // Offset of 16-byte chunk c of row r in a piece's keys (or values): boxes of
@@ -330,7 +337,6 @@ struct MmaPieces {
   __device__ __forceinline__ void open(const AttendArgs& a, int b, int h) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = a.G;
     const float qscale = a.scale * kLog2e;
-    vref = 7.8886091e-31f; vmul = 64.f / vref;      // 2^-100
     // chunks 4 apart (keys) and 2 apart (values) differ in bits that the rows'
     // swizzle leaves in place: the rest of a load's address is a constant
 #pragma unroll
@@ -487,22 +493,7 @@ struct MmaPieces {
       for (int i = 1; i < 2 * NB; ++i) top[r] = fmaxf(top[r], x[r][i]);
       raise |= top[r] > m[r] + kRaise;
     }
-    float vtop = 0.f;
-    if constexpr (E4M3) {
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) vtop = fmaxf(vtop, fmaxf(vf[nb].x, vf[nb].y));
-      raise |= vtop >= 2.f * vref;
-    }
     if (__any_sync(0xffffffffu, raise)) {
-      float fall = 1.f;
-      if constexpr (E4M3) {
-        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 1));
-        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, 2));
-        const float v1 = fmaxf(vref, __uint_as_float(__float_as_uint(vtop) & 0x7f800000u));
-        fall = vref / v1;
-        vref = v1;
-        vmul = 64.f / v1;
-      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float y = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
@@ -512,7 +503,7 @@ struct MmaPieces {
         m[r] = m1;
         l[r] *= c;
         // accumulator columns 2t, 2t + 1 belong to rows 2t, 2t + 1
-        const float c0 = __shfl_sync(0xffffffffu, c, 8 * t) * fall, c1 = __shfl_sync(0xffffffffu, c, 8 * t + 4) * fall;
+        const float c0 = __shfl_sync(0xffffffffu, c, 8 * t), c1 = __shfl_sync(0xffffffffu, c, 8 * t + 4);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           acc[r][k][0] *= c0; acc[r][k][1] *= c1;
@@ -528,19 +519,12 @@ struct MmaPieces {
         float p0 = ex2(x[r][2 * nb] - mu), p1 = ex2(x[r][2 * nb + 1] - mu);
         l[r] += p0 + p1;
         if constexpr (E4M3) {
-          p0 *= vf[nb].x * vmul;
-          p1 *= vf[nb].y * vmul;
+          p0 *= vf[nb].x;
+          p1 *= vf[nb].y;
         }
-        uint32_t hi, lo;
-        if constexpr (E4M3) {
-          hi = pack_f16(p0, p1);
-          const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-          lo = pack_f16(p0 - hf.x, p1 - hf.y);
-        } else {
-          hi = pack_bf16(p0, p1);
-          const float2 hf = bf2_to_f2(hi);
-          lo = pack_bf16(p0 - hf.x, p1 - hf.y);
-        }
+        const uint32_t hi = pack_bf16(p0, p1);
+        const float2 hf = bf2_to_f2(hi);
+        const uint32_t lo = pack_bf16(p0 - hf.x, p1 - hf.y);
         if (GP == 4) {
           ph[r][nb] = lane < 16 ? hi : lo;     // rows 4..7 repeat the heads: they carry the low terms
         } else {
@@ -571,12 +555,13 @@ struct MmaPieces {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             // bytes: two keys' elements 2g, 2g + 1 -> the keys' pairs of element 2g (row g) and of 2g + 1 (row g + 8)
-            const uint32_t u = __byte_perm(f[2 * c], 0, 0x3120), w = __byte_perm(f[2 * c + 1], 0, 0x3120);
-            const uint32_t v[4] = {e4m3_to_f16(u), e4m3_to_f16_high(u), e4m3_to_f16(w), e4m3_to_f16_high(w)};
+            uint32_t v[4];
+            e4m3_to_bf16(f[2 * c], v[0], v[1]);
+            e4m3_to_bf16(f[2 * c + 1], v[2], v[3]);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-              mma_f16_16816(acc[r][k + c], v, ph[r][2 * p], ph[r][2 * p + 1]);
-              if (GP != 4) mma_f16_16816(acc[r][k + c], v, pl[r][2 * p], pl[r][2 * p + 1]);
+              mma_bf16_16816(acc[r][k + c], v, ph[r][2 * p], ph[r][2 * p + 1]);
+              if (GP != 4) mma_bf16_16816(acc[r][k + c], v, pl[r][2 * p], pl[r][2 * p + 1]);
             }
           }
         }
@@ -597,12 +582,6 @@ struct MmaPieces {
         o[0] = m[r]; o[1] = l[r]; o[2] = any ? 1.f : 0.f;
       }
       if (any) {
-        if constexpr (E4M3) {
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[r][k][i] *= vref * (1.f / 64.f);
-        }
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           // element of head dimension that accumulator rows g and g + 8 hold

@@ -536,6 +536,32 @@ def test_attend_long_and_many(dtype, cache, d, g, hkv, page):
             check_attend(out[i], lse[i], q[i], x[:, :, 0], x[:, :, 1], dtype)
 
 
+@pytest.mark.parametrize("dtype,cache,d,g,hkv,page", [("bf16", "e4m3", 128, 4, 2, 16), ("bf16", "e4m3", 128, 8, 1, 64),
+                                                      ("bf16", "e4m3", 128, 16, 1, 16), ("bf16", "e4m3", 64, 3, 2, 32),
+                                                      ("bf16", "e4m3", 64, 16, 1, 32), ("bf16", "native", 128, 4, 2, 16)])
+@pytest.mark.parametrize("exponent,below", [(20, 35.0), (28, 45.0), (40, 80.0), (40, 10.0), (-40, -20.0)])
+@pytest.mark.parametrize("n", [30, 2900])
+def test_attend_values_of_unlike_magnitudes(dtype, cache, d, g, hkv, page, exponent, below, n):
+    """One value row 2^exponent times the others, half of it zeros, whose score
+    lies `below` the others' (far below: no weight; a little below: most of the
+    output; above them and small: none of it): first, in the middle and last."""
+    spots = [0, n // 2, n - 1]
+    c, table, q = filled([n] * 3, g * hkv, hkv, d, page, dtype, cache, seed=n + abs(exponent))
+    base = torch.ones(d, device="cuda")
+    q = (base * (1 + torch.arange(g * hkv, device="cuda").view(1, -1, 1) / 32)).expand(3, -1, -1).to(q.dtype).contiguous()
+    k, v = rows((3, n, hkv, d), dtype, 5, 0.25), rows((3, n, hkv, d), dtype, 6)
+    for b, at in enumerate(spots):
+        k[b, at] = (k[b, at].float() - base * (below / d ** 0.5)).to(k.dtype)
+        v[b, at] *= 2.0 ** exponent
+        v[b, at, :, 1::2] = 0
+    c.append(0, k, v, ints(slots_of(table, [n] * 3, page, n)))
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    c.attend(0, q, ints(table), ints([n] * 3), out, lse)
+    for b in range(3):
+        x = held_rows(c, 0, table, n, page, b)
+        check_attend(out[b], lse[b], q[b], x[:, :, 0], x[:, :, 1], dtype)
+
+
 @pytest.mark.parametrize("dtype,cache,hq,hkv", [("bf16", "native", 600, 600), ("bf16", "e4m3", 460, 460), ("f32", "native", 500, 500),
                                                  ("bf16", "native", 96, 6)])
 def test_attend_more_heads_than_the_gpu_has_blocks(dtype, cache, hq, hkv):
