@@ -225,7 +225,10 @@ int kvpop_create(const kvpop_config* cfg, void* dev_mem, size_t bytes, kvpop_han
     }
   }
   uint8_t* m = h->mem;
-  bool ok = cudaMemset(m + L.kv_off, 0, cfg->n_layers * L.kv_stride) == cudaSuccess &&
+  // Non-blocking streams do not order the default stream's work behind theirs: what is queued there, and may still
+  // write to memory that an allocator has handed on, ends first.
+  bool ok = cudaDeviceSynchronize() == cudaSuccess &&
+            cudaMemset(m + L.kv_off, 0, cfg->n_layers * L.kv_stride) == cudaSuccess &&
             cudaMemset(m + L.pos_off, 0xff, cfg->n_layers * L.pos_stride) == cudaSuccess &&
             cudaMemset(m + L.score_off, 0, cfg->n_layers * L.score_stride) == cudaSuccess &&
             cudaMemset(m + L.state_off, 0, L.total - L.state_off) == cudaSuccess;

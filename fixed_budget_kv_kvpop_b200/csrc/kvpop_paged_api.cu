@@ -230,6 +230,9 @@ int kvpop_paged_create(const kvpop_paged_config* cfg, void* dev_mem, size_t byte
   for (int l = 0; ok && l < cfg->n_layers; ++l)
     ok = make_attend_map(&h->maps[l], h->mem + L.pages_off + l * L.pages_stride, cfg->dtype, cfg->head_dim, e8,
                          cfg->page_size, static_cast<int64_t>(cfg->n_pages) * cfg->n_kv_heads) == 0;
+  // The default stream's clearing does not wait for non-blocking streams: what is queued there, and may still write
+  // to memory that an allocator has handed on, ends first.
+  ok = ok && cudaDeviceSynchronize() == cudaSuccess;
   if (!ok || cudaMemset(h->mem, 0, L.total) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     delete h;
     return KVPOP_ERR_CUDA;

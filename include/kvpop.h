@@ -23,7 +23,8 @@
  *    lifetime (the cache buffer).
  *  - Work is asynchronous on the caller's CUDA stream (`stream`, a
  *    cudaStream_t; NULL = legacy default stream).  Only kvpop_create,
- *    kvpop_inspect and kvpop_get_error synchronise.
+ *    kvpop_inspect, kvpop_get_error, kvpop_paged_create and
+ *    kvpop_paged_get_error synchronise.
  *  - Calls on one handle must be ordered on one stream (or by the caller's
  *    events): the handle's split-K scratch is shared by its layers.
  *  - All batch rows share one sequence length.  Layers are independent and
@@ -171,7 +172,7 @@ int kvpop_cache_bytes(const kvpop_config* cfg, size_t* bytes);
 
 /* Binds a caller-allocated device buffer (>= kvpop_cache_bytes, 256-byte
  * aligned, on the current device) and initialises it (empty cache,
- * synchronously).  The buffer must outlive the handle.  *out receives the
+ * synchronously, after all work queued on the device).  The buffer must outlive the handle.  *out receives the
  * handle (host memory owned by the library until kvpop_destroy).
  * Page §3 "Fixed-budget pruning" (a hard, fixed-size cache: eviction is
  * permanent, so the cache never grows past its budget) and §C.1 (the budget
@@ -470,8 +471,8 @@ typedef struct kvpop_paged_layout_info {
 int kvpop_paged_bytes(const kvpop_paged_config* cfg, size_t* bytes);
 
 /* Binds a caller-allocated buffer (>= kvpop_paged_bytes, 256-byte aligned, on
- * the current device) and clears it to zero, synchronously.  The buffer must
- * outlive the handle.  Errors as kvpop_create. */
+ * the current device) and clears it to zero, synchronously, after all
+ * work queued on the device.  The buffer must outlive the handle.  Errors as kvpop_create. */
 int kvpop_paged_create(const kvpop_paged_config* cfg, void* dev_mem, size_t bytes, kvpop_paged_handle** out);
 
 /* Writes keys and values of batch * n_tokens tokens into layer `layer`.

@@ -706,6 +706,51 @@ def test_a_step_in_a_graph_with_growing_lengths():
     assert torch.equal(caches[0].pages(0).view(torch.uint8), caches[1].pages(0).view(torch.uint8))
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "budget"])
+def test_a_cache_made_in_memory_that_a_stream_still_writes(kind):
+    """On a side stream torch hands a freed block on while work queued there may
+    still write to it: a cache made in it begins empty all the same."""
+    if kind == "budget":
+        cfg = kp.make_config(batch=2, n_layers=2, n_q_heads=8, n_kv_heads=2, head_dim=128, sinks=4, window=32, topk=64,
+                             max_prefill_chunk=256, external_scores=True)
+        make, nbytes = (lambda: kp.KVPopCache(cfg)), kp.cache_bytes(cfg)
+    else:
+        lens, page, hkv, d = [2900, 40], 16, 2, 128
+        table, n_pages = tables(lens, page, 1)
+        cfg = kp.make_paged_config(n_layers=1, n_q_heads=8, n_kv_heads=hkv, head_dim=d, page_size=page, n_pages=n_pages,
+                                   max_batch=64, cache="native" if kind == "bf16" else kind)
+        make, nbytes = (lambda: kp.KVPopPagedCache(cfg)), kp.paged_bytes(cfg)
+        x = [rows((2, 2900, hkv, d), "bf16", i) for i in (2, 3)]
+        slots, q = ints(slots_of(table, lens, page, 2900)), rows((2, 8, d), "bf16", 4)
+        tab, n = ints(table), ints(lens)
+    quiet = make()
+    side = torch.cuda.Stream()
+    big = torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        block = torch.empty(nbytes + 256, dtype=torch.uint8, device="cuda")
+        at = block.data_ptr()
+        for i in range(60):          # 10 ms or more of work before the block is written
+            big.fill_(i)
+        block.fill_(0x55)
+        del block
+        late = make()
+        assert late.buffer.data_ptr() == at      # the same memory
+    for c in (quiet, late):
+        start = (-c.buffer.data_ptr()) % 256
+        c.held = c.buffer[start:start + nbytes]
+    torch.cuda.synchronize()
+    assert torch.equal(quiet.held, late.held)
+    if kind != "budget":
+        assert not late.held.any()
+        outs = []
+        for c in (quiet, late):
+            c.append(0, *x, slots)
+            outs.append(torch.empty_like(q))
+            c.attend(0, q, tab, n, outs[-1])
+        assert torch.equal(*outs)
+
+
 def test_two_caches_on_two_streams():
     """Calls of two objects overlap on two streams and keep their results."""
     args = [filled([3000, 500], 8, 2, 128, 64, "bf16", "native", seed=s) for s in (1, 2)]
