@@ -4,7 +4,9 @@ Argument marshalling only: every step of the decode path runs in the CUDA
 kernels behind include/kvpop.h.  The paged calls are marshalled by _binding
 (csrc/binding.cpp), the others by ctypes.  PyTorch supplies device memory and streams.
 Importing this module loads the in-tree libkvpop.so and fails loudly if it is
-missing; there is no fallback implementation.
+missing; there is no fallback implementation.  _binding.so, which is built for
+one torch and one Python, is loaded when a Rope or a KVPopPagedCache is made,
+and that fails loudly without it; the fixed-budget calls do not need it.
 
 Names follow the C ABI: kvpop_cache_bytes, kvpop_create, kvpop_prefill,
 kvpop_decode_step, kvpop_inspect, kvpop_get_layout, kvpop_get_error,
@@ -16,11 +18,10 @@ The paged cache's calls (kvpop_paged_*) are methods of `KVPopPagedCache`;
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import struct
 from typing import Optional
-
-import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # KVPOP_LIBRARY may point at another build of the same library (e.g. a tuning variant).
@@ -163,10 +164,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
 
 lib = load_library()
 
-try:
-    from . import _binding
-except ImportError as e:
-    raise ImportError(f"{_HERE}/_binding.so does not load ({e}): run `python fixed_budget_kv_kvpop_b200/csrc/build.py`") from e
+
+def _load_binding():
+    """Loads _binding.so, which from then on is this module's attribute _binding."""
+    import torch  # noqa: F401  (its libraries come first)
+    try:
+        return importlib.import_module(__name__ + "._binding")
+    except ImportError as e:
+        raise ImportError(f"{_HERE}/_binding.so does not load ({e}): run "
+                          "`python fixed_budget_kv_kvpop_b200/csrc/build.py`") from e
+
+
+def __getattr__(name):
+    if name == "_binding":
+        return _load_binding()
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _addresses(library) -> dict:
@@ -476,6 +488,7 @@ class Rope:
     its tensors alive.  Made by make_rope."""
 
     def __init__(self, inv_freq, q_weight, k_weight, eps, scale, interleaved):
+        _load_binding()
         self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight
         self.device = inv_freq.device
         self.rot_dim = 2 * inv_freq.numel()
@@ -493,6 +506,7 @@ def make_rope(inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6, scal
     weights, or None for heads that are not normalised.  eps is added to the
     mean square; scale multiplies cosine and sine.  interleaved: pairs
     (2i, 2i + 1) instead of (i, i + rot_dim / 2)."""
+    import torch
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.device.type != "cuda":
         raise ValueError("inv_freq: expected a cuda tensor")
     if inv_freq.dim() != 1 or inv_freq.numel() % 4:
@@ -521,7 +535,8 @@ def qk_norm_rope(rope: Rope, q, k, positions, q_out, k_out, stream=None) -> None
     heads; any strides of whole 16 bytes (views of a projection's output,
     transposed views of head-major buffers), q_out = q and k_out = k among
     them.  positions: int32 [batch][tokens]."""
-    _check(_binding.qk_norm_rope(_FN["kvpop_qk_norm_rope"], _rope_args(rope), q, k, positions, q_out, k_out, stream),
+    args = _rope_args(rope)
+    _check(_binding.qk_norm_rope(_FN["kvpop_qk_norm_rope"], args, q, k, positions, q_out, k_out, stream),
            "kvpop_qk_norm_rope")
 
 
@@ -550,6 +565,8 @@ class KVPopPagedCache:
     events."""
 
     def __init__(self, cfg: kvpop_paged_config, device=None, library=None):
+        _load_binding()
+        import torch
         self.cfg = cfg
         self._lib = library or lib
         self.nbytes = paged_bytes(cfg, self._lib)
@@ -639,5 +656,6 @@ class KVPopPagedCache:
 
     def clear_error(self, stream=None):
         if stream is None:
+            import torch
             stream = torch.cuda.current_stream(self.device)
         _check(self._lib.kvpop_paged_clear_error(self.handle, stream.cuda_stream), "kvpop_paged_clear_error")

@@ -1,6 +1,9 @@
 """Paged cache and heads: the oracle's own checks, and every refusal that needs no GPU."""
 import ctypes
+import os
 import struct
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -329,3 +332,46 @@ def test_blocks_of_a_window(kb):
     """A window of w tokens touches at most w / kb + 2 blocks, wherever it ends."""
     for w in range(1, 300):
         assert max((n + kb - 1) // kb - max(n - w, 0) // kb for n in range(1, 400)) <= w // kb + 2
+
+
+# ---- what the package needs to load ----
+
+@pytest.mark.parametrize("without", ["torch", "binding", "broken binding"])
+def test_the_fixed_budget_calls_need_neither_torch_nor_the_binding(tmp_path, without):
+    """_binding.so is built for one torch and one Python: without it, or without
+    torch, the package loads and its ctypes calls work; the paged ones say what is missing."""
+    package = tmp_path / "fixed_budget_kv_kvpop_b200"
+    package.mkdir()
+    (package / "__init__.py").write_text(open(kp.__file__).read())
+    if without == "broken binding":
+        (package / "_binding.so").write_bytes(b"built for another Python")
+    code = """
+import sys
+if WITHOUT == "torch":
+    sys.modules["torch"] = None
+import fixed_budget_kv_kvpop_b200 as kp
+cfg = kp.make_config(batch=1, n_layers=1, n_q_heads=8, n_kv_heads=2, head_dim=128, sinks=4, window=16, topk=16,
+                     external_scores=True)
+assert kp.cache_bytes(cfg) > 0
+paged = kp.make_paged_config(n_layers=1, n_q_heads=8, n_kv_heads=2, head_dim=128, page_size=16, n_pages=4, max_batch=1)
+assert kp.paged_bytes(paged) > 0
+for make in (lambda: kp.KVPopPagedCache(paged), lambda: kp.Rope(None, None, None, 0.0, 1.0, False), lambda: kp._binding):
+    try:
+        make()
+    except ImportError as e:
+        assert "torch" in str(e) if WITHOUT == "torch" else "build.py" in str(e), e
+    else:
+        raise AssertionError("made without its binding")
+try:
+    kp.qk_norm_rope(None, None, None, None, None, None)
+except ValueError as e:
+    assert "make_rope" in str(e)
+try:
+    kp.nothing
+except AttributeError as e:
+    assert "nothing" in str(e)
+print("ok")
+"""
+    env = {**os.environ, "KVPOP_LIBRARY": kp.LIB_PATH, "PYTHONPATH": str(tmp_path)}
+    r = subprocess.run([sys.executable, "-c", f"WITHOUT = {without!r}" + code], capture_output=True, text=True, env=env, cwd=tmp_path)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr
