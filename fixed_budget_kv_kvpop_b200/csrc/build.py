@@ -12,7 +12,8 @@ PKG = os.path.dirname(HERE)
 ROOT = os.path.dirname(PKG)
 SOURCES = ["kvpop_api.cu", "kvpop_decode.cu", "kvpop_prefill.cu", "kvpop_prefill_attn.cu", "kvpop_mlstm.cu",
            "kvpop_paged_api.cu", "kvpop_paged.cu", "kvpop_paged_attn.cu"]
-HEADERS = ["kvpop_internal.cuh", "kvpop_prefill_attn.cuh", "kvpop_paged.cuh", os.path.join(ROOT, "include", "kvpop.h")]
+HEADERS = ["kvpop_internal.cuh", "kvpop_prefill_attn.cuh", "kvpop_paged.cuh",
+           "kvpop_paged_split.cuh", os.path.join(ROOT, "include", "kvpop.h")]
 OUT = os.path.join(PKG, "libkvpop.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",

@@ -22,6 +22,7 @@
 // block into it by tensor copies (one instruction per 16 keys and values) and
 // computes on the oldest.  Warps meet once per item, to join their sums.
 #include "kvpop_paged.cuh"
+#include "kvpop_paged_split.cuh"
 
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -31,15 +32,6 @@ namespace kvpop {
 namespace {
 
 constexpr int NW = 4;                    // warps per CTA
-constexpr int kMinShare = 8;             // blocks of a part at least (1 x 1024 tokens: 4 12.9 us, 8 11.7 us, 16 12.4 us, 32 17.3 us)
-// If there are more sequences than groups and none has more tokens than this, they go to single warps.  Few long ones
-// would leave warps idle (8 groups of 4 heads, bf16: 64 x 200 19 us against 25, 64 x 300 27 either way, 256 x 300 69
-// against 66; e4m3 64 x 400 34 against 30), the sooner the more a warp has to compute (fp32 on the FMA units, 8 groups
-// of 16 heads: 80 x 60 48 us against 60, 80 x 250 151 against 104).
-constexpr int solo_tokens(bool f32) { return f32 ? 64 : 256; }
-// Largest part that is taken for one part of one sequence per group, when equal
-// ranges would have `even` blocks: ranges cost a second item and its join.
-__host__ __device__ constexpr int64_t most_of(int64_t even) { return even + even / 5 + 16; }
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRaise = 8.f;            // a running maximum moves when a score passes it by this (in powers of two)
 
@@ -90,165 +82,69 @@ __device__ __forceinline__ void e4m3_to_bf16(uint32_t x, uint32_t& even, uint32_
   odd = __byte_perm(__float_as_uint(a.y), __float_as_uint(b.y), 0x7632);
 }
 
-// a / b for a >= 0, b > 0: in 32 bits where a allows, a fraction of the 64-bit division's time.
-__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
-  if ((a >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
-// The sequences and how their work is split.  Kept in shared memory, one copy
-// per warp: the function that finds items reads it from there, where an
-// argument struct passed on by address costs a trip to global memory.
-struct Split {
-  const int32_t* lens;
-  int64_t total;     // blocks of all sequences
-  int batch, Hkv, window, fixed;   // as AttendArgs
-  int cap;           // tokens that a row of the page table can name
-  int share;         // blocks of a range
-  int groups;        // groups of CTAs
-  int aligned;       // one part of one sequence per group
-  int solo;          // whole sequences of one head, each by a warp of its own
+// The lanes of a warp, for the split's arithmetic.  nb0: blocks of sequence `lane`.
+template <typename Sum>
+struct LaneWarp {
+  using Lanes = int;
+  struct Hit {
+    int lane, own;
+    int64_t sum;     // up to the lane, or (not found) of all
+  };
+  int nb0;
+  template <typename F> __device__ __forceinline__ int lanes(F f) const { return f(static_cast<int>(threadIdx.x & 31)); }
+  template <typename F> __device__ __forceinline__ int cached(F) const { return nb0; }
+  template <typename F> __device__ __forceinline__ int each(int v, F f) const { return f(v); }
+  __device__ __forceinline__ int64_t sum(int v) const { return __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v)); }
+  __device__ __forceinline__ int top(int v) const { return __reduce_max_sync(0xffffffffu, v); }
+  __device__ __forceinline__ int some(int v) const { return __popc(__ballot_sync(0xffffffffu, v > 0)); }
+  __device__ __forceinline__ bool find(int v, int64_t before, int64_t target, bool many, Hit& hit) const {
+    const int lane = threadIdx.x & 31;
+    Sum sum = v;
+    if (many) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const Sum u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
+      }
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + static_cast<int64_t>(sum) > target);
+    hit.lane = past ? __ffs(past) - 1 : 31;
+    hit.own = __shfl_sync(0xffffffffu, v, hit.lane);
+    hit.sum = static_cast<int64_t>(__shfl_sync(0xffffffffu, sum, hit.lane));
+    return past != 0;
+  }
 };
 
-// Attended tokens [lo, n) of a sequence whose length is given as n; lengths outside the table are cut.
-struct Span {
-  int lo, n;
-};
-__device__ __forceinline__ Span span_of(const Split& sp, int n) {
-  n = n < 0 ? 0 : min(n, sp.cap);
-  return Span{sp.window > 0 && n > sp.window ? n - sp.window : 0, n};
+// The whole warp's next item, made by its first lane.
+template <typename F>
+__device__ __forceinline__ void put_item(Item* it, F make) {
+  __syncwarp();                      // the old item has been read
+  if ((threadIdx.x & 31) == 0) *it = make();
+  __syncwarp();
 }
-// Blocks of sequence b.
-template <int KB>
-__device__ __forceinline__ int blocks_of(const Split& sp, int b) {
-  const Span s = span_of(sp, sp.lens[b]);
-  return (s.n + KB - 1) / KB - s.lo / KB;
-}
-
-// An item: blocks of one sequence and head.  Each warp keeps two in shared
-// memory, the one it computes on and the one it copies for, so that they take
-// no registers in the loops.
-struct Item {
-  int b, h;
-  int lo, n;         // the sequence's attended tokens
-  int j, jend;       // blocks [j, jend) of the item; block x holds tokens x KB .. x KB + KB - 1
-  int first, parts;  // groups that hold a part of the sequence
-  int second;        // 1: in the first of them it is not the range's first sequence
-  int left;          // blocks of the range from this item on
-  int64_t pos;       // of the item's first block among all blocks (ranges)
-};
-
-// The item of a group where parts are fixed: kMinShare blocks of one sequence.
+// The item of a group where parts are fixed.
 template <int KB>
 __device__ __forceinline__ bool fixed_item(const Split& sp, Item* it, int grp, int h) {
-  const int b = grp / sp.fixed, part = grp - b * sp.fixed;
-  const Span s = span_of(sp, sp.lens[b]);
-  const int j0 = s.lo / KB, nb = (s.n + KB - 1) / KB - j0;
-  if (part * kMinShare >= nb) return false;
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) {
-    const int j = j0 + part * kMinShare, jend = min(j + kMinShare, j0 + nb);
-    *it = Item{b, h, s.lo, s.n, j, jend, grp - part, (nb + kMinShare - 1) / kMinShare, 0, jend - j, 0};
-  }
-  __syncwarp();
+  Item x;
+  if (!fixed_part<KB>(sp, grp, h, x)) return false;
+  put_item(it, [&] { return x; });
   return true;
 }
-
 // The warp's first or next item where warps take one sequence and head each (pos: which).
 template <int KB>
 __device__ __noinline__ bool solo_item(const Split* spp, Item* it, bool start) {
-  const Split& sp = *spp;
-  const int warps = gridDim.x * NW, units = sp.batch * sp.Hkv;
-  int u = start ? static_cast<int>(blockIdx.x) * NW + static_cast<int>(threadIdx.x) / 32 : static_cast<int>(it->pos) + warps;
-  int b = 0, nb = 0;
-  for (;; u += warps) {
-    if (u >= units) return false;
-    b = u / sp.Hkv;
-    nb = blocks_of<KB>(sp, b);
-    if (nb > 0) break;
-  }
-  const Span s = span_of(sp, sp.lens[b]);
-  const int j0 = s.lo / KB;
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) *it = Item{b, u - b * sp.Hkv, s.lo, s.n, j0, j0 + nb, 0, 1, 0, nb, u};
-  __syncwarp();
+  const int warps = gridDim.x * NW;
+  Item x;
+  if (!solo_part<KB>(*spp, start ? static_cast<int>(blockIdx.x) * NW + static_cast<int>(threadIdx.x) / 32 : static_cast<int>(it->pos) + warps, warps, x))
+    return false;
+  put_item(it, [&] { return x; });
   return true;
 }
-
-// The CTA's first or next item (the whole warp together); false at the end.
-// CTAs take one head, or with more heads than CTAs every gridDim.x-th.  nb0:
-// blocks of sequence `lane`.
+// The CTA's first or next item; false at the end.  nb0: blocks of sequence `lane`.
 template <int KB>
 __device__ __noinline__ bool next_item(const Split* spp, Item* it, int nb0, bool start) {
-  const Split& sp = *spp;
-  const int lane = threadIdx.x & 31, Hkv = sp.Hkv, n_cta = gridDim.x;
-  const bool many = Hkv > n_cta;
-  const int grp = many ? 0 : static_cast<int>(blockIdx.x) / Hkv;
-  int b = 0, h, parts = 1, skip = 0, left;
-  int64_t pos = 0;
-  if (!start && it->left > it->jend - it->j) {       // the range goes on in the next sequence that has blocks
-    h = it->h;
-    left = it->left - (it->jend - it->j);
-    pos = it->pos + (it->jend - it->j);
-    b = it->b;
-    do ++b; while (blocks_of<KB>(sp, b) == 0);
-  } else {
-    h = start ? (many ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) - grp * Hkv) : it->h + n_cta;
-    if (h >= Hkv || grp >= sp.groups) return false;
-    if (sp.fixed > 0) return fixed_item<KB>(sp, it, grp, h);
-    // the sequence in which the range begins
-    const int64_t target = sp.aligned ? grp : static_cast<int64_t>(grp) * sp.share;
-    int64_t before = 0;
-    for (int b0 = 0;; b0 += 32) {
-      if (b0 >= sp.batch) return false;
-      int own = 0;
-      if (b0 + lane < sp.batch) own = b0 == 0 ? nb0 : blocks_of<KB>(sp, b0 + lane);
-      if (sp.aligned) own = static_cast<int>(static_cast<uint32_t>(own + sp.share - 1) / static_cast<uint32_t>(sp.share));
-      uint32_t sum = own;            // 32 sequences of at most 2^26 blocks
-      if (sp.batch > 1) {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
-          if (lane >= o) sum += u;
-        }
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, before + sum > target);
-      if (past) {
-        const int i = __ffs(past) - 1;
-        b = b0 + i;
-        parts = __shfl_sync(0xffffffffu, own, i);
-        skip = static_cast<int>(target - before - (__shfl_sync(0xffffffffu, sum, i) - static_cast<uint32_t>(parts)));
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    pos = target;
-    left = static_cast<int>(min(static_cast<int64_t>(sp.share), sp.total - target));
-  }
-  __syncwarp();                      // the old item has been read
-  if (lane == 0) {
-    const Span s = span_of(sp, sp.lens[b]);
-    const int j0 = s.lo / KB, nb = (s.n + KB - 1) / KB - j0;
-    Item x;
-    x.b = b; x.h = h; x.lo = s.lo; x.n = s.n; x.pos = pos;
-    if (sp.aligned) {         // part `skip`
-      x.j = j0 + skip * sp.share;
-      x.jend = min(x.j + sp.share, j0 + nb);
-      x.left = x.jend - x.j;
-      x.first = grp - skip; x.parts = parts; x.second = 0;
-    } else {
-      x.j = j0 + skip;
-      x.jend = min(j0 + nb, x.j + left);
-      x.left = left;
-      const int64_t beg = pos - skip;                // of the sequence
-      x.first = static_cast<int>(quotient(beg, sp.share));
-      x.parts = static_cast<int>(quotient(beg + nb - 1, sp.share)) - x.first + 1;
-      x.second = beg != static_cast<int64_t>(x.first) * sp.share;
-    }
-    *it = x;
-  }
-  __syncwarp();
-  return true;
+  LaneWarp<BlockSum<KB>> w{nb0};
+  return next_part<KB>(w, *spp, *it, start, blockIdx.x, gridDim.x, [&](auto make) { put_item(it, make); });
 }
 
 // What a warp's ring holds.  A block is NSUB pieces of KEYS keys and values;
@@ -278,13 +174,6 @@ struct Geo {
   static_assert(NST >= 1, "a warp needs a stage");
   static constexpr int SMEM = 1024 + NW * NST * (STAGE + SCALE + 16) + MERGE + WEIGHTS + 256;
 };
-
-// A range begins in one sequence and ends in another, so a group leaves at
-// most two partials per head: that of its range's first sequence, and another.
-// Partial i of an item's sequence: by group, and whether its range begins with this sequence.
-__device__ __forceinline__ int64_t slot_of(const Item& x, int i, int Hkv) {
-  return static_cast<int64_t>(2 * (x.first + i) + (i == 0 ? x.second : 0)) * Hkv + x.h;
-}
 
 struct AttendScratch {
   float* acc;        // [2 kAttendRanges][G][D]
@@ -810,7 +699,7 @@ __device__ __forceinline__ void attend_items(const CUtensorMap& map, const Atten
   } else if (spp->aligned && a.batch <= 32 && n_cta >= Hkv) {
     // what next_item does, from what the lanes already have
     const int grp = blockIdx.x / Hkv;
-    const int own = static_cast<int>(static_cast<uint32_t>(nb0 + spp->share - 1) / static_cast<uint32_t>(spp->share));
+    const int own = parts_of(nb0, spp->share);
     int sum = own;
     if (a.batch > 1) {
 #pragma unroll
@@ -1056,7 +945,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
   Split sp;
   sp.lens = a.lens;
   sp.batch = a.batch; sp.Hkv = Hkv; sp.window = a.window; sp.fixed = a.fixed;
-  sp.cap = static_cast<int>(min(static_cast<int64_t>(a.width) << a.pg.page_shift, static_cast<int64_t>(1 << 30)));
+  sp.cap = static_cast<int>(min(static_cast<int64_t>(a.width) << a.pg.page_shift, kMostTokens));
   sp.groups = max(1, n_cta / Hkv);
   sp.total = 0; sp.share = kMinShare; sp.aligned = 0; sp.solo = 0;
   int nb0 = 0;             // blocks of sequence `lane`
@@ -1067,61 +956,16 @@ attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ A
       if (given != span_of(sp, given).n) set_error(a.pg.err, DEVERR_BAD_INDEX);
     }
   } else {
-    int64_t total = 0;
-    int longest = 0, seqs = 0;
     bool bad_len = false;
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      const int b = b0 + lane;
-      int nb = 0;
-      Span s{0, 0};
-      if (b < a.batch) {
-        const int given = a.lens[b];
-        s = span_of(sp, given);
-        nb = (s.n + KB - 1) / KB - s.lo / KB;
-        bad_len |= given != s.n;
-      }
-      if (b0 == 0) {
-        nb0 = nb;
+    LaneWarp<BlockSum<KB>> w{0};
+    split_work<KB>(w, sp, G_::F32, [&](int b, int nb, const Span& s, int given) {
+      if (b < 32) {
+        w.nb0 = nb0 = nb;
         span0 = s;
       }
-      total += __reduce_add_sync(0xffffffffu, static_cast<unsigned>(nb));     // 32 sequences of at most 2^26 blocks
-      longest = max(longest, __reduce_max_sync(0xffffffffu, nb));
-      seqs += __popc(__ballot_sync(0xffffffffu, nb > 0));
-    }
+      bad_len |= given != s.n;
+    });
     if (bad_len && blockIdx.x == 0 && warp == 0) set_error(a.pg.err, DEVERR_BAD_INDEX);
-    sp.total = total;
-    const int64_t even = quotient(total + sp.groups - 1, sp.groups);
-    sp.share = static_cast<int>(min(max(even, static_cast<int64_t>(kMinShare)), static_cast<int64_t>(1 << 30)));
-    if (longest * KB <= solo_tokens(G_::F32) && seqs > sp.groups) {
-      sp.solo = 1;
-    } else if (seqs > 0 && seqs <= sp.groups) {
-      // the smallest largest part with which there are no more parts than groups
-      auto fits = [&](int s) {
-        int items = 0;
-        for (int b0 = 0; b0 < a.batch; b0 += 32) {
-          int nb = 0;
-          if (b0 + lane < a.batch) nb = b0 == 0 ? nb0 : blocks_of<KB>(sp, b0 + lane);
-          const int np = static_cast<int>(static_cast<uint32_t>(nb + s - 1) / static_cast<uint32_t>(s));
-          items += __reduce_add_sync(0xffffffffu, min(np, sp.groups + 1));
-        }
-        return items <= sp.groups;
-      };
-      const int per = sp.groups / seqs;
-      int lo = sp.share, hi = (longest + per - 1) / per;     // hi fits: no sequence has more than `per` parts
-      if (hi <= lo || fits(lo)) {
-        hi = lo;
-      } else {
-        while (hi - lo > 1 + lo / 32) {
-          const int mid = lo + (hi - lo) / 2;
-          if (fits(mid)) hi = mid;
-          else lo = mid;
-        }
-      }
-      if (hi <= most_of(sp.share)) {
-        sp.aligned = 1;
-        sp.share = hi;
-      }
-    }
   }
   if (lane == 0) sh.split[warp] = sp;
   __syncwarp();
@@ -1200,15 +1044,11 @@ int launch_attend(const CUtensorMap& map, const AttendArgs& a, void* scratch, in
   sc.ml = sc.acc + static_cast<size_t>(kAttendRanges) * 2 * a.G * d;
   sc.ticket = reinterpret_cast<int32_t*>(sc.ml + static_cast<size_t>(kAttendRanges) * 2 * a.G * 4);
   return with_kernel(dtype, d, e8, a.G, [&](auto kernel, int smem, int ctas, int KB) {
-    // as many CTAs as fit the GPU, and no more than the longest sequences that the tables can name would take
-    int64_t most = ctas * num_sms < kAttendRanges ? ctas * num_sms : kAttendRanges;
-    int64_t blocks = ((static_cast<int64_t>(a.width) << a.pg.page_shift) + KB - 1) / KB;
-    if (a.window > 0 && a.window / KB + 2 < blocks) blocks = a.window / KB + 2;     // a window may begin and end inside a block
-    const int64_t need = a.pg.Hkv * a.batch * ((blocks + kMinShare - 1) / kMinShare);
+    const Launch x = launch_of(ctas * num_sms < kAttendRanges ? ctas * num_sms : kAttendRanges,
+                               static_cast<int64_t>(a.width) << a.pg.page_shift, KB, a.window, a.pg.Hkv, a.batch);
     AttendArgs b = a;
-    b.fixed = need >= 1 && need <= most ? static_cast<int>((blocks + kMinShare - 1) / kMinShare) : 0;
-    const int grid = static_cast<int>(need < 1 ? 1 : need < most ? need : most);
-    return launch_dependent(kernel, dim3(grid), NW * 32, smem, st, map, b, sc);
+    b.fixed = x.fixed;
+    return launch_dependent(kernel, dim3(x.grid), NW * 32, smem, st, map, b, sc);
   });
 }
 
