@@ -94,7 +94,11 @@ struct LaneWarp {
   template <typename F> __device__ __forceinline__ int lanes(F f) const { return f(static_cast<int>(threadIdx.x & 31)); }
   template <typename F> __device__ __forceinline__ int cached(F) const { return nb0; }
   template <typename F> __device__ __forceinline__ int each(int v, F f) const { return f(v); }
-  __device__ __forceinline__ int64_t sum(int v) const { return __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v)); }
+  __device__ __forceinline__ int few(int v) const { return __reduce_add_sync(0xffffffffu, v); }
+  __device__ __forceinline__ int64_t sum(int v) const {
+    if (sizeof(Sum) == 4) return __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v));
+    return (static_cast<int64_t>(few(v >> 16)) << 16) + few(v & 0xffff);
+  }
   __device__ __forceinline__ int top(int v) const { return __reduce_max_sync(0xffffffffu, v); }
   __device__ __forceinline__ int some(int v) const { return __popc(__ballot_sync(0xffffffffu, v > 0)); }
   __device__ __forceinline__ bool find(int v, int64_t before, int64_t target, bool many, Hit& hit) const {
@@ -699,7 +703,7 @@ __device__ __forceinline__ void attend_items(const CUtensorMap& map, const Atten
   } else if (spp->aligned && a.batch <= 32 && n_cta >= Hkv) {
     // what next_item does, from what the lanes already have
     const int grp = blockIdx.x / Hkv;
-    const int own = parts_of(nb0, spp->share);
+    const int own = parts_of(nb0, static_cast<int>(spp->share));
     int sum = own;
     if (a.batch > 1) {
 #pragma unroll
@@ -711,7 +715,8 @@ __device__ __forceinline__ void attend_items(const CUtensorMap& map, const Atten
     const unsigned past = __ballot_sync(0xffffffffu, sum > grp);
     some = past != 0 && grp < spp->groups;
     if (some && lane == __ffs(past) - 1) {
-      const int part = grp - (sum - own), j0 = span0.lo / KB, j = j0 + part * spp->share, jend = min(j + spp->share, j0 + nb0);
+      const int part = grp - (sum - own), share = static_cast<int>(spp->share), j0 = span0.lo / KB;
+      const int j = j0 + part * share, jend = min(j + share, j0 + nb0);
       items[warp][0] = Item{lane, static_cast<int>(blockIdx.x) - grp * Hkv, span0.lo, span0.n, j, jend, grp - part, own, 0, jend - j, 0};
     }
     __syncwarp();

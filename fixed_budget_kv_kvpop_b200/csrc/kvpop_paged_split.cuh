@@ -6,12 +6,14 @@
 //   lanes(f)               f(lane) of each lane
 //   each(v, f)             f of each lane's value
 //   sum(v), top(v)         over the lanes
+//   few(v)                 sum(v) where 32 bits hold it
 //   some(v)                how many lanes are above 0
 //   find(v, before, target, many, hit)   whether before + the sum of v passes target, and at which lane first; many: v
 //                          may be above 0 past the first lane
 //   cached(f)              lanes(f) of the first 32 sequences' blocks, which the caller may have
 #pragma once
 #include <cstdint>
+#include <type_traits>
 
 #ifdef __CUDACC__
 #define KVPOP_HD __host__ __device__ __forceinline__
@@ -35,9 +37,9 @@ KVPOP_HD int64_t most_of(int64_t even) { return even + even / 5 + 16; }
 template <typename T> KVPOP_HD T lesser(T a, T b) { return a < b ? a : b; }
 template <typename T> KVPOP_HD T greater(T a, T b) { return a > b ? a : b; }
 
-// a / b for a >= 0, b > 0: in 32 bits where a allows, a fraction of the 64-bit division's time.
-KVPOP_HD int64_t quotient(int64_t a, int b) {
-  if ((a >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+// a / b for a >= 0, b > 0: in 32 bits where they allow, a fraction of the 64-bit division's time.
+KVPOP_HD int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
   return a / b;
 }
 KVPOP_HD int parts_of(int blocks, int share) {
@@ -49,11 +51,11 @@ KVPOP_HD int parts_of(int blocks, int share) {
 // argument struct passed on by address costs a trip to global memory.
 struct Split {
   const int32_t* lens;
-  int64_t total;     // blocks of all sequences
+  int64_t total;     // blocks of all sequences: at most 2^37
+  int64_t share;     // blocks of a range
   int batch, Hkv, window;
   int fixed;         // > 0: parts of kMinShare blocks, this many groups of CTAs for each sequence
   int cap;           // tokens that a row of the page table can name
-  int share;         // blocks of a range
   int groups;        // groups of CTAs
   int aligned;       // one part of one sequence per group
   int solo;          // whole sequences of one head, each by a warp of its own
@@ -69,7 +71,7 @@ KVPOP_HD Span span_of(const Split& sp, int n) {
 }
 // A sum of blocks over 32 sequences.
 template <int KB>
-using BlockSum = uint32_t;
+using BlockSum = std::conditional_t<32 * (kMostTokens / KB) <= UINT32_MAX, uint32_t, uint64_t>;
 // Blocks of sequence b.
 template <int KB>
 KVPOP_HD int blocks_of(const Split& sp, int b) {
@@ -86,7 +88,7 @@ struct Item {
   int j, jend;       // blocks [j, jend) of the item; block x holds tokens x KB .. x KB + KB - 1
   int first, parts;  // groups that hold a part of the sequence
   int second;        // 1: in the first of them it is not the range's first sequence
-  int left;          // blocks of the range from this item on
+  int64_t left;      // blocks of the range from this item on
   int64_t pos;       // of the item's first block among all blocks (ranges)
 };
 
@@ -126,7 +128,7 @@ KVPOP_HD void split_work(W& w, Split& sp, bool f32, F see) {
   }
   sp.total = total;
   const int64_t even = quotient(total + sp.groups - 1, sp.groups);
-  sp.share = static_cast<int>(lesser(greater(even, static_cast<int64_t>(kMinShare)), kMostTokens));
+  sp.share = greater(even, static_cast<int64_t>(kMinShare));
   if (longest * KB <= solo_tokens(f32) && seqs > sp.groups) {
     sp.solo = 1;
   } else if (seqs > 0 && seqs <= sp.groups) {
@@ -136,12 +138,13 @@ KVPOP_HD void split_work(W& w, Split& sp, bool f32, F see) {
       for (int b0 = 0; b0 < sp.batch; b0 += 32) {
         auto count = [&](int lane) { return b0 + lane < sp.batch ? blocks_of<KB>(sp, b0 + lane) : 0; };
         const auto nb = b0 == 0 ? w.cached(count) : w.lanes(count);
-        items += static_cast<int>(w.sum(w.each(nb, [&](int x) { return lesser(parts_of(x, s), sp.groups + 1); })));
+        items += w.few(w.each(nb, [&](int x) { return lesser(parts_of(x, s), sp.groups + 1); }));
       }
       return items <= sp.groups;
     };
     const int per = sp.groups / seqs;
-    int lo = sp.share, hi = (longest + per - 1) / per;     // hi fits: no sequence has more than `per` parts
+    // (no more sequences than groups: no share above the longest)
+    int lo = static_cast<int>(sp.share), hi = (longest + per - 1) / per;     // hi fits: no sequence has more than `per` parts
     if (hi <= lo || fits(lo)) {
       hi = lo;
     } else {
@@ -160,8 +163,8 @@ KVPOP_HD void split_work(W& w, Split& sp, bool f32, F see) {
 
 // Where an item lies: block `skip` of sequence b (or, aligned, its part `skip` of `parts`), head h.
 struct Place {
-  int b, h, parts, skip, left;
-  int64_t pos;
+  int b, h, parts, skip;
+  int64_t left, pos;
 };
 
 // The item of a group where parts are fixed: kMinShare blocks of one sequence.
@@ -201,18 +204,19 @@ KVPOP_HD Item item_at(const Split& sp, const Place& p, int grp) {
   Item x;
   x.b = p.b; x.h = p.h; x.lo = s.lo; x.n = s.n; x.pos = p.pos;
   if (sp.aligned) {         // part `skip`
-    x.j = j0 + p.skip * sp.share;
-    x.jend = lesser(x.j + sp.share, j0 + nb);
+    const int share = static_cast<int>(sp.share);
+    x.j = j0 + p.skip * share;
+    x.jend = lesser(x.j + share, j0 + nb);
     x.left = x.jend - x.j;
     x.first = grp - p.skip; x.parts = p.parts; x.second = 0;
   } else {
     x.j = j0 + p.skip;
-    x.jend = lesser(j0 + nb, x.j + p.left);
+    x.jend = static_cast<int>(lesser(static_cast<int64_t>(j0 + nb), x.j + p.left));
     x.left = p.left;
     const int64_t beg = p.pos - p.skip;              // of the sequence
     x.first = static_cast<int>(quotient(beg, sp.share));
     x.parts = static_cast<int>(quotient(beg + nb - 1, sp.share)) - x.first + 1;
-    x.second = beg != static_cast<int64_t>(x.first) * sp.share;
+    x.second = beg != x.first * sp.share;
   }
   return x;
 }
@@ -240,17 +244,17 @@ KVPOP_HD bool next_part(W& w, const Split& sp, const Item& it, bool start, int c
     return true;
   }
   // the sequence in which the range begins
-  const int64_t target = sp.aligned ? grp : static_cast<int64_t>(grp) * sp.share;
+  const int64_t target = sp.aligned ? grp : grp * sp.share;
   int64_t before = 0;
   for (int b0 = 0;; b0 += 32) {
     if (b0 >= sp.batch) return false;
     auto count = [&](int lane) { return b0 + lane < sp.batch ? blocks_of<KB>(sp, b0 + lane) : 0; };
     auto own = b0 == 0 ? w.cached(count) : w.lanes(count);
-    if (sp.aligned) own = w.each(own, [&](int nb) { return parts_of(nb, sp.share); });
+    if (sp.aligned) own = w.each(own, [&](int nb) { return parts_of(nb, static_cast<int>(sp.share)); });
     typename W::Hit hit;
     if (w.find(own, before, target, sp.batch > 1, hit)) {
       const Place x{b0 + hit.lane, h, hit.own, static_cast<int>(target - before - (hit.sum - hit.own)),
-                    static_cast<int>(lesser(static_cast<int64_t>(sp.share), sp.total - target)), target};
+                    lesser(sp.share, sp.total - target), target};
       put([&] { return item_at<KB>(sp, x, grp); });
       return true;
     }

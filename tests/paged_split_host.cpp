@@ -28,6 +28,11 @@ struct LoopWarp {
     for (int x : v) s += x;
     return static_cast<int64_t>(s);
   }
+  int few(const Lanes& v) const {
+    int s = 0;
+    for (int x : v) s += x;
+    return s;
+  }
   int top(const Lanes& v) const {
     int m = v[0];
     for (int x : v) m = x > m ? x : m;

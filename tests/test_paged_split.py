@@ -26,7 +26,7 @@ def lib(tmp_path_factory):
 def items(lib, lens, hkv, kb, most, tokens, window=0, f32=False):
     """Rows (cta, warp, b, h, j, jend, first, parts, slot, at) and what the split chose."""
     lens = np.ascontiguousarray(lens, np.int32)
-    room = 200000
+    room = 400000
     out, how = np.zeros((room, 10), np.int64), np.zeros(7, np.int64)
     P64, P32 = ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int32)
     n = lib.split_items(kb, int(f32), lens.ctypes.data_as(P32), len(lens), hkv, window, ctypes.c_int64(tokens), most, WARPS,
@@ -101,3 +101,21 @@ def test_short_sequences_go_to_single_warps(lib, hkv, batch, kb, f32):
     assert per.max() - per.min() <= 1
     lens[rng.random(batch) < 0.3] = 0
     check(lib, lens, hkv, kb, 444, 4096, f32=f32)
+
+
+@pytest.mark.parametrize("kb,batch,hkv,most", [(8, 32, 8, 444), (8, 64, 1, 296), (16, 64, 1, 296), (8, 1024, 8, 444), (16, 1024, 8, 444),
+                                               (64, 1024, 300, 444), (16, 40, 300, 444), (8, 33, 8, 444)])
+def test_the_longest_sequences(lib, kb, batch, hkv, most):
+    """2^30 tokens in every sequence (their tables may share pages): 2^27 blocks of 8 tokens each, 2^32 of 32 sequences."""
+    rows, how = check(lib, [MOST] * batch, hkv, kb, most, MOST, f32=kb == 8)
+    assert how["total"] == batch * (MOST // kb)
+    assert how["groups"] * how["share"] >= how["total"] or how["aligned"]
+    lens = np.full(batch, MOST)
+    lens[::3] = np.arange(len(lens[::3])) * 1000
+    check(lib, lens, hkv, kb, most, MOST, f32=kb == 8)
+
+
+def test_the_longest_window(lib):
+    for kb in (8, 16, 32, 64):
+        check(lib, [MOST, 5, MOST - 7], 2, kb, 444, MOST, window=2 ** 31 - 1)
+        check(lib, [MOST] * 40, 8, kb, 444, MOST, window=MOST // 2 + 1, f32=kb == 8)
