@@ -21,6 +21,7 @@ import ctypes
 import importlib
 import os
 import struct
+import sys
 from typing import Optional
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -167,9 +168,12 @@ lib = load_library()
 
 def _load_binding():
     """Loads _binding.so, which from then on is this module's attribute _binding."""
-    import torch  # noqa: F401  (its libraries come first)
+    import torch  # (its libraries come first)
     try:
-        return importlib.import_module(__name__ + "._binding")
+        m = importlib.import_module(__name__ + "._binding")
+        if (m.TORCH, m.PYTHON) != (torch.__version__.split("+")[0], sys.hexversion >> 16):
+            raise ImportError(f"built for torch {m.TORCH} and Python {m.PYTHON >> 8}.{m.PYTHON & 255}")
+        return m
     except ImportError as e:
         raise ImportError(f"{_HERE}/_binding.so does not load ({e}): run "
                           "`python fixed_budget_kv_kvpop_b200/csrc/build.py`") from e

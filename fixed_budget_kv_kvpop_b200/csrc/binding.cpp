@@ -11,6 +11,7 @@
 
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include "../../include/kvpop.h"
 
@@ -329,4 +330,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+// Tells the loader which torch and Python it was compiled for.
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && (PyModule_AddStringConstant(m, "TORCH", TORCH_VERSION) < 0 || PyModule_AddIntConstant(m, "PYTHON", PY_VERSION_HEX >> 16) < 0)) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -70,14 +70,13 @@ def build(force: bool = False, verbose: bool = False, out: str = OUT, defines=()
 
 BINDING_SOURCE = os.path.join(HERE, "binding.cpp")
 BINDING_OUT = os.path.join(PKG, "_binding.so")
+BINDING_STAMP = os.path.join(PKG, "_binding.txt")
 
 
 def build_binding(force: bool = False) -> str:
     """Compiles the Python side of the paged calls (host code only) against
-    the torch and Python that run this."""
-    deps = [BINDING_SOURCE, os.path.join(ROOT, "include", "kvpop.h"), __file__]
-    if not force and os.path.exists(BINDING_OUT) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING_OUT) for p in deps):
-        return BINDING_OUT
+    the torch and Python that run this, and keeps what it was built for beside
+    it (_binding.txt): another torch, Python or command builds it again."""
     import sysconfig
     import torch
     home = os.path.dirname(torch.__file__)
@@ -87,11 +86,18 @@ def build_binding(force: bool = False) -> str:
            "-I" + os.path.join(home, "include"), "-I" + os.path.join(home, "include", "torch", "csrc", "api", "include"),
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), BINDING_SOURCE,
            "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-o", BINDING_OUT + ".tmp"]
+    built_for = "\n".join([torch.__version__, torch.version.git_version, sys.version, sysconfig.get_config_var("SOABI") or "", *cmd])
+    deps = [BINDING_SOURCE, os.path.join(ROOT, "include", "kvpop.h"), __file__]
+    if not force and os.path.exists(BINDING_OUT) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING_OUT) for p in deps):
+        if os.path.exists(BINDING_STAMP) and open(BINDING_STAMP).read() == built_for:
+            return BINDING_OUT
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError("g++ failed building _binding.so")
     os.replace(BINDING_OUT + ".tmp", BINDING_OUT)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(built_for)
     return BINDING_OUT
 
 

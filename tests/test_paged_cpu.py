@@ -1,5 +1,6 @@
 """Paged cache and heads: the oracle's own checks, and every refusal that needs no GPU."""
 import ctypes
+import importlib.util
 import os
 import struct
 import subprocess
@@ -375,3 +376,43 @@ print("ok")
     env = {**os.environ, "KVPOP_LIBRARY": kp.LIB_PATH, "PYTHONPATH": str(tmp_path)}
     r = subprocess.run([sys.executable, "-c", f"WITHOUT = {without!r}" + code], capture_output=True, text=True, env=env, cwd=tmp_path)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr
+
+
+@pytest.mark.parametrize("change", ["nothing", "torch", "python", "compiler", "source"])
+def test_the_binding_is_built_again_for_another_torch_or_python(tmp_path, monkeypatch, change):
+    """_binding.so reads torch's and Python's structures as they were when it was compiled."""
+    spec = importlib.util.spec_from_file_location("kvpop_build", os.path.join(os.path.dirname(kp.__file__), "csrc", "build.py"))
+    build = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(build)
+    monkeypatch.setattr(build, "BINDING_OUT", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(build, "BINDING_STAMP", str(tmp_path / "_binding.txt"), raising=False)
+    runs = []
+
+    def compiler(cmd, **kw):
+        runs.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    build.build_binding()
+    build.build_binding()
+    assert len(runs) == 1
+    if change == "torch":
+        monkeypatch.setattr(torch, "__version__", "0.0")
+    elif change == "python":
+        monkeypatch.setattr(sys, "version", "0.0")
+    elif change == "compiler":
+        monkeypatch.setenv("CXX", "another")
+    elif change == "source":
+        os.utime(build.BINDING_OUT, (0, 0))
+    build.build_binding()
+    assert len(runs) == (1 if change == "nothing" else 2)
+    build.build_binding()
+    assert len(runs) == (1 if change == "nothing" else 2)
+
+
+@pytest.mark.parametrize("what,value", [("TORCH", "1.0.0"), ("PYTHON", 0x0301)])
+def test_a_binding_of_another_torch_or_python_is_refused(monkeypatch, what, value):
+    monkeypatch.setattr(kp._binding, what, value)
+    with pytest.raises(ImportError, match="built for .* 1.0.0|built for .*Python 3.1.*build.py"):
+        kp.Rope(None, None, None, 0.0, 1.0, False)
