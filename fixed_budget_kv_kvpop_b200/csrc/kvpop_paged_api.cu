@@ -122,7 +122,14 @@ int sm_count(int device) {
   return sms;
 }
 
-int status_of(int r) { return r == 0 ? KVPOP_OK : r == -2 ? KVPOP_ERR_BAD_SHAPE : KVPOP_ERR_CUDA; }
+// A CUDA call failed.  Its error is taken back: it belongs to this call alone, and the fixed-budget calls ask for the
+// thread's last error after their launches.
+int cuda_failed() {
+  cudaGetLastError();
+  return KVPOP_ERR_CUDA;
+}
+
+int status_of(int r) { return r == 0 ? KVPOP_OK : r == -2 ? KVPOP_ERR_BAD_SHAPE : cuda_failed(); }
 
 }  // namespace
 
@@ -187,9 +194,9 @@ int kvpop_qk_norm_rope(int32_t dtype, int32_t head_dim, int32_t n_q_heads, int32
   int device = 0;
   if (!device_of(q->data, &device)) return KVPOP_ERR_INVALID_ARG;
   DeviceScope scope(device);
-  if (!scope.ok()) return KVPOP_ERR_CUDA;
+  if (!scope.ok()) return cuda_failed();
   const int sms = sm_count(device);
-  if (sms == 0) return KVPOP_ERR_CUDA;
+  if (sms == 0) return cuda_failed();
   a.pos = positions;
   a.batch = batch; a.n_tokens = n_tokens; a.Hq = n_q_heads; a.Hkv = n_kv_heads;
   return status_of(launch_heads(a, dtype, head_dim, HEADS_DENSE, sms, static_cast<cudaStream_t>(stream)));
@@ -212,10 +219,10 @@ int kvpop_paged_create(const kvpop_paged_config* cfg, void* dev_mem, size_t byte
   if (!dev_mem || bytes < L.total || !aligned(dev_mem, 256)) return KVPOP_ERR_INVALID_ARG;
   int dev = 0, at = 0;
   if (!device_of(dev_mem, &at)) return KVPOP_ERR_INVALID_ARG;
-  if (cudaGetDevice(&dev) != cudaSuccess) return KVPOP_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed();
   if (at != dev) return KVPOP_ERR_INVALID_ARG;
   const int sms = sm_count(dev);
-  if (sms == 0) return KVPOP_ERR_CUDA;
+  if (sms == 0) return cuda_failed();
   kvpop_paged_handle* h = new (std::nothrow) kvpop_paged_handle();
   if (!h) return KVPOP_ERR_INVALID_ARG;
   h->cfg = *cfg;
@@ -235,7 +242,7 @@ int kvpop_paged_create(const kvpop_paged_config* cfg, void* dev_mem, size_t byte
   ok = ok && cudaDeviceSynchronize() == cudaSuccess;
   if (!ok || cudaMemset(h->mem, 0, L.total) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     delete h;
-    return KVPOP_ERR_CUDA;
+    return cuda_failed();
   }
   *out = h;
   return KVPOP_OK;
@@ -257,7 +264,7 @@ int kvpop_paged_append(kvpop_paged_handle* h, int32_t layer, const kvpop_rows* k
   a.slots = slots;
   a.batch = batch; a.n_tokens = n_tokens; a.Hq = c.n_q_heads; a.Hkv = c.n_kv_heads;
   DeviceScope scope(h->device);
-  if (!scope.ok()) return KVPOP_ERR_CUDA;
+  if (!scope.ok()) return cuda_failed();
   return status_of(launch_heads(a, c.dtype, c.head_dim, HEADS_APPEND, h->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -284,7 +291,7 @@ int kvpop_paged_append_qkv(kvpop_paged_handle* h, int32_t layer, const kvpop_rop
   a.slots = slots;
   a.batch = batch; a.n_tokens = n_tokens; a.Hq = c.n_q_heads; a.Hkv = c.n_kv_heads;
   DeviceScope scope(h->device);
-  if (!scope.ok()) return KVPOP_ERR_CUDA;
+  if (!scope.ok()) return cuda_failed();
   return status_of(launch_heads(a, c.dtype, c.head_dim, HEADS_STEP, h->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -305,7 +312,7 @@ int kvpop_paged_gather(kvpop_paged_handle* h, int32_t layer, const int32_t* page
   a.table = page_table; a.lens = lens; a.table_stride = table_stride;
   a.batch = batch; a.width = table_width; a.n_tokens = n_tokens;
   DeviceScope scope(h->device);
-  if (!scope.ok()) return KVPOP_ERR_CUDA;
+  if (!scope.ok()) return cuda_failed();
   return status_of(launch_gather(a, c.dtype, c.head_dim, static_cast<cudaStream_t>(stream)));
 }
 
@@ -330,7 +337,7 @@ int kvpop_paged_attend(kvpop_paged_handle* h, int32_t layer, const void* q, cons
   a.softcap = o.softcap;
   a.window = o.window;
   DeviceScope scope(h->device);
-  if (!scope.ok()) return KVPOP_ERR_CUDA;
+  if (!scope.ok()) return cuda_failed();
   return status_of(launch_attend(h->maps[layer], a, h->mem + h->lay.scratch_off, c.dtype, c.head_dim,
                                  h->num_sms, static_cast<cudaStream_t>(stream)));
 }
@@ -345,9 +352,9 @@ int kvpop_paged_get_layout(const kvpop_paged_handle* h, kvpop_paged_layout_info*
 int kvpop_paged_get_error(kvpop_paged_handle* h, int32_t* device_bits) {
   if (!h) return KVPOP_ERR_INVALID_ARG;
   DeviceScope scope(h->device);
-  if (!scope.ok() || cudaDeviceSynchronize() != cudaSuccess) return KVPOP_ERR_CUDA;
+  if (!scope.ok() || cudaDeviceSynchronize() != cudaSuccess) return cuda_failed();
   int32_t bits = 0;
-  if (cudaMemcpy(&bits, h->mem + h->lay.err_off, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return KVPOP_ERR_CUDA;
+  if (cudaMemcpy(&bits, h->mem + h->lay.err_off, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return cuda_failed();
   if (device_bits) *device_bits = bits;
   if (bits == 0) return KVPOP_OK;
   return (bits & DEVERR_TIMEOUT) ? KVPOP_ERR_TIMEOUT : KVPOP_ERR_DEVICE;
@@ -356,10 +363,10 @@ int kvpop_paged_get_error(kvpop_paged_handle* h, int32_t* device_bits) {
 int kvpop_paged_clear_error(kvpop_paged_handle* h, void* stream) {
   if (!h) return KVPOP_ERR_INVALID_ARG;
   DeviceScope scope(h->device);
-  if (!scope.ok()) return KVPOP_ERR_CUDA;
+  if (!scope.ok()) return cuda_failed();
   return cudaMemsetAsync(h->mem + h->lay.err_off, 0, 4, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? KVPOP_OK
-             : KVPOP_ERR_CUDA;
+             : cuda_failed();
 }
 
 int kvpop_paged_destroy(kvpop_paged_handle* h) {

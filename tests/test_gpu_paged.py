@@ -861,6 +861,31 @@ def test_calls_from_two_threads():
         assert all(pool.map(work, range(2)))
 
 
+def test_a_failed_paged_call_leaves_no_error_behind():
+    """A paged call that CUDA refuses (here: a clearing while a stream captures)
+    reports it, and the next calls, paged and fixed-budget, do not."""
+    hq, hkv, d = 8, 2, 128
+    budget = kp.KVPopCache(kp.make_config(batch=1, n_layers=1, n_q_heads=hq, n_kv_heads=hkv, head_dim=d, sinks=4, window=32,
+                                          topk=32, external_scores=True))
+    c, table, q = filled([40], hq, hkv, d, 16, "bf16", "native")
+    out, tab, lens = torch.empty_like(q), ints(table), ints([40])
+    k, score = rows((1, hkv, d), "bf16", 1), torch.ones(1, hkv, device="cuda")
+    cfg = kp.make_paged_config(n_layers=1, n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=16, n_pages=4, max_batch=1)
+    mem = torch.empty(kp.paged_bytes(cfg), dtype=torch.uint8, device="cuda")
+    rt = ctypes.CDLL("libcudart.so.12")
+    side, graph, handle = torch.cuda.Stream(), ctypes.c_void_p(), ctypes.c_void_p()
+    torch.cuda.synchronize()
+    assert rt.cudaStreamBeginCapture(ctypes.c_void_p(side.cuda_stream), 0) == 0
+    status = kp.lib.kvpop_paged_create(ctypes.byref(cfg), mem.data_ptr(), mem.numel(), ctypes.byref(handle))
+    rt.cudaStreamEndCapture(ctypes.c_void_p(side.cuda_stream), ctypes.byref(graph))
+    rt.cudaGetLastError()
+    assert status == kp.KVPOP_ERR_CUDA and not handle.value
+    budget.decode_append(0, k, k, ext_score=score)
+    budget.decode_attend(0, q, out)
+    c.attend(0, q, tab, lens, out)
+    assert budget.get_error() == c.get_error() == (kp.KVPOP_OK, 0)
+
+
 def test_refusals_on_the_gpu():
     c = cache_of(4, 2, 64, 16, 4, max_batch=2)
     k = rows((1, 3, 2, 64), "bf16", 1)
