@@ -369,8 +369,9 @@ struct MmaPieces {
       for (int i = 0; i < 2 * NB; ++i) {
         float y = s[i >> 1][0][2 * r + (i & 1)];
         if (CHAINS == 2) y += s[i >> 1][CHAINS - 1][2 * r + (i & 1)];
-        if constexpr (E4M3) y *= (i & 1) ? kf[i >> 1].y : kf[i >> 1].x;
-        x[r][i] = y * qmul[r];
+        // (the two factors first: the sum times a large key's scale alone may pass fp32)
+        if constexpr (E4M3) x[r][i] = y * (((i & 1) ? kf[i >> 1].y : kf[i >> 1].x) * qmul[r]);
+        else x[r][i] = y * qmul[r];
       }
       if (a.softcap > 0.f) {
 #pragma unroll

@@ -562,6 +562,20 @@ def test_attend_values_of_unlike_magnitudes(dtype, cache, d, g, hkv, page, expon
         check_attend(out[b], lse[b], q[b], x[:, :, 0], x[:, :, 1], dtype)
 
 
+@pytest.mark.parametrize("dtype,cache,d,g,hkv,page", [SHAPES[0], SHAPES[5], SHAPES[6], SHAPES[7], SHAPES[9]])
+@pytest.mark.parametrize("ek,eq,scale", [(-90, 90, 0.25), (20, -20, 0.25), (110, -110, 0.25), (118, -98, 2.0 ** -22), (-60, -20, 2.0 ** 78)])
+def test_attend_large_keys_and_small_queries(dtype, cache, d, g, hkv, page, ek, eq, scale):
+    """Keys of 2^ek and queries of 2^eq times the ordinary have ordinary scores under a scale that makes up for them."""
+    n = 300
+    c, table, q = filled([n], g * hkv, hkv, d, page, dtype, cache, seed=4)
+    q *= 2.0 ** eq
+    c.append(0, rows((1, n, hkv, d), dtype, 5, 2.0 ** ek), rows((1, n, hkv, d), dtype, 6), ints(slots_of(table, [n], page, n)))
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    c.attend(0, q, ints(table), ints([n]), out, lse, scale=scale)
+    x = held_rows(c, 0, table, n, page, 0)
+    check_attend(out[0], lse[0], q[0], x[:, :, 0], x[:, :, 1], dtype, scale)
+
+
 @pytest.mark.parametrize("dtype,cache,hq,hkv", [("bf16", "native", 600, 600), ("bf16", "e4m3", 460, 460), ("f32", "native", 500, 500),
                                                  ("bf16", "native", 96, 6)])
 def test_attend_more_heads_than_the_gpu_has_blocks(dtype, cache, hq, hkv):
