@@ -151,6 +151,23 @@ __device__ __noinline__ bool next_item(const Split* spp, Item* it, int nb0, bool
   return next_part<KB>(w, *spp, *it, start, blockIdx.x, gridDim.x, [&](auto make) { put_item(it, make); });
 }
 
+// An item that is a part of its sequence, kept until the parts are joined.
+struct Part {
+  int b, h, first, parts, second;    // as Item
+};
+// Shared memory of a CTA beside its rings, the accumulators to join and the weights.
+template <int GP, int NST>
+struct AttendShared {
+  uint64_t bars[NW][NST];
+  Split split[NW];
+  Item items[NW][2];
+  float ml[NW][GP][2];     // each warp's running maxima and sums
+  int32_t any[NW];         // whether it saw a key
+  Part open[2];
+  int32_t last[2];
+  int32_t live[NW][NST];   // pieces that were copied into a stage
+};
+
 // What a warp's ring holds.  A block is NSUB pieces of KEYS keys and values;
 // a piece comes by one tensor copy (bf16, e4m3) or two plain ones (fp32).
 template <typename T, int D, bool E4M3, int GP>
@@ -165,18 +182,28 @@ struct Geo {
   static constexpr int ROWB = D * ES < 128 ? D * ES : 128;   // bytes of a row in one box of a tensor copy
   static constexpr int HALVES = D * ES / ROWB;
   static constexpr int SCALE = E4M3 ? NSUB * 128 : 0;        // bytes of scales of a stage
-  static constexpr int MERGE = NW * GP * (D + 4) * 4;
+  static constexpr int MERGE = NW * GP * D * 4;              // accumulators that the warps of a CTA join
   static constexpr int WEIGHTS = F32 ? NW * KEYS * 16 : 0;   // fp32: weights of a piece for four heads
   // CTAs per SM.  More warps hide the chain from a block's arrival to its sums,
   // up to where registers run out or power does: 64 x 8192 bf16 takes 338, 327
   // and 314 us with 2, 3 and 4 CTAs in a short run, but 339, 336 and 359 us in
   // a long one, where the GPU holds its 1000 W by its clock
   static constexpr int CTAS = GP > 4 ? 2 : F32 ? (D == 64 ? 3 : 2) : 3;
-  static constexpr int CTA = (228 * 1024) / CTAS - 1024;
-  static constexpr int NST0 = (CTA - 1024 - MERGE - WEIGHTS - 512) / (NW * (STAGE + SCALE + 16));
-  static constexpr int NST = NST0 > 8 ? 8 : NST0;
-  static_assert(NST >= 1, "a warp needs a stage");
-  static constexpr int SMEM = 1024 + NW * NST * (STAGE + SCALE + 16) + MERGE + WEIGHTS + 256;
+  // Stages of a warp's ring: as many as fit, two at least, so that a copy is on its way while a warp computes
+  // (32 x 32768 e4m3 with four heads, where two just fit: 240 us, 264 us with one).  1 KB of each CTA's share is the system's.
+  static constexpr int smem(int nst) {
+    return (NW * nst * (STAGE + SCALE) + MERGE + WEIGHTS + static_cast<int>(sizeof(AttendShared<GP, 1>)) + NW * (nst - 1) * 12 + 127) & ~127;
+  }
+  static constexpr int stages() {
+    int n = 8;
+    while (n > 0 && CTAS * (smem(n) + 1024) > 228 * 1024) --n;
+    return n;
+  }
+  static constexpr int NST = stages();
+  static constexpr int SMEM = smem(NST);
+  using Shared = AttendShared<GP, NST>;
+  static_assert(NST >= 2, "a warp needs two stages");
+  static_assert(NW * NST * (STAGE + SCALE) + MERGE + WEIGHTS + static_cast<int>(sizeof(Shared)) <= SMEM, "shared memory of a CTA");
 };
 
 struct AttendScratch {
@@ -464,7 +491,7 @@ struct MmaPieces {
   }
 
   // Accumulators, running maxima and sums of this warp to shared memory.
-  __device__ __forceinline__ void close(float* macc, float* mml, int warp, bool any) {
+  __device__ __forceinline__ void close(float* macc, float (*ml)[2], int warp, bool any) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -472,8 +499,7 @@ struct MmaPieces {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       const int row = g + 8 * r;
       if (t == 0 && row < GP) {
-        float* o = mml + (warp * GP + row) * 4;
-        o[0] = m[r]; o[1] = l[r]; o[2] = any ? 1.f : 0.f;
+        ml[row][0] = m[r]; ml[row][1] = l[r];
       }
       if (any) {
 #pragma unroll
@@ -637,7 +663,7 @@ struct FmaPieces {
     }
   }
 
-  __device__ __forceinline__ void close(float* macc, float* mml, int warp, bool any) {
+  __device__ __forceinline__ void close(float* macc, float (*ml)[2], int warp, bool any) {
     const int lane = threadIdx.x & 31, part = lane & 7;
     const int head = ((part >> 2) & 1) * 2 + ((part >> 1) & 1);
 #pragma unroll
@@ -646,8 +672,7 @@ struct FmaPieces {
       s += __shfl_xor_sync(0xffffffffu, s, 8);
       s += __shfl_xor_sync(0xffffffffu, s, 16);
       if (lane < 8 && !(part & 1)) {
-        float* o = mml + (warp * GP + 4 * c + head) * 4;
-        o[0] = m[c]; o[1] = s; o[2] = any ? 1.f : 0.f;
+        ml[4 * c + head][0] = m[c]; ml[4 * c + head][1] = s;
       }
       if (any) {
 #pragma unroll
@@ -659,16 +684,10 @@ struct FmaPieces {
   }
 };
 
-struct AttendShared {
-  Split split[NW];
-  Item items[NW][2], open[2];
-  int last[2];
-};
-
 // The kernel after the split.  SOLO: warps take whole sequences and heads, and no two warps meet.
 template <typename C, bool SOLO>
 __device__ __forceinline__ void attend_items(const CUtensorMap& map, const AttendArgs& a, const AttendScratch& sc,
-                                             AttendShared& sh, int nb0, Span span0, uint8_t* smem) {
+                                             typename C::Geometry::Shared& sh, int nb0, Span span0, uint8_t* smem) {
   using G_ = typename C::Geometry;
   using T = typename C::Elements;
   constexpr int D = C::kD, GP = C::kGP, KB = G_::KB, NSUB = G_::NSUB, NST = G_::NST;
@@ -678,10 +697,9 @@ __device__ __forceinline__ void attend_items(const CUtensorMap& map, const Atten
   uint8_t* ring = smem + warp * NST * G_::STAGE;
   uint8_t* sring = smem + NW * NST * G_::STAGE + warp * NST * G_::SCALE;
   float* macc = reinterpret_cast<float*>(smem + NW * NST * (G_::STAGE + G_::SCALE));   // [NW][GP][D]
-  float* mml = macc + NW * GP * D;                                                // [NW][GP][4]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(mml + NW * GP * 4) + warp * NST;
-  int32_t* live = reinterpret_cast<int32_t*>(reinterpret_cast<uint64_t*>(mml + NW * GP * 4) + NW * NST) + warp * NST;
-  float* wbuf = reinterpret_cast<float*>(smem + G_::SMEM - 1024 - 256 - G_::WEIGHTS) + warp * (G_::WEIGHTS / (4 * NW));
+  float* wbuf = macc + NW * GP * D + warp * (G_::WEIGHTS / (4 * NW));
+  uint64_t* bars = sh.bars[warp];
+  int32_t* live = sh.live[warp];
   auto& items = sh.items;
   const int Hkv = a.pg.Hkv, G = a.G, n_cta = gridDim.x;
   // sequences without a token
@@ -826,7 +844,8 @@ __device__ __forceinline__ void attend_items(const CUtensorMap& map, const Atten
     }
 
     // ---- join the warps ----
-    c.close(macc, mml, warp, any);
+    c.close(macc, sh.ml[warp], warp, any);
+    if (lane == 0) sh.any[warp] = any;
     if constexpr (SOLO) __syncwarp();
     else __syncthreads();
     const bool complete = SOLO || w.parts == 1;
@@ -838,8 +857,8 @@ __device__ __forceinline__ void attend_items(const CUtensorMap& map, const Atten
 #pragma unroll
       for (int x = 0; x < NW; ++x) {
         if (SOLO && x != warp) continue;
-        M = fmaxf(M, mml[(x * GP + q) * 4]);
-        seen += mml[(x * GP + q) * 4 + 2];
+        M = fmaxf(M, sh.ml[x][q][0]);
+        seen += sh.any[x];
       }
       const float mu = M == -INFINITY ? 0.f : M;
       float L = 0.f;
@@ -847,10 +866,10 @@ __device__ __forceinline__ void attend_items(const CUtensorMap& map, const Atten
 #pragma unroll
       for (int x = 0; x < NW; ++x) {
         if (SOLO && x != warp) continue;
-        if (mml[(x * GP + q) * 4 + 2] == 0.f) continue;
-        const float c = ex2(mml[(x * GP + q) * 4] - mu);
+        if (!sh.any[x]) continue;
+        const float c = ex2(sh.ml[x][q][0] - mu);
         const float4 v = *reinterpret_cast<const float4*>(&macc[(x * GP + q) * D + e]);
-        L = fmaf(c, mml[(x * GP + q) * 4 + 1], L);
+        L = fmaf(c, sh.ml[x][q][1], L);
         o.x = fmaf(c, v.x, o.x); o.y = fmaf(c, v.y, o.y); o.z = fmaf(c, v.z, o.z); o.w = fmaf(c, v.w, o.w);
       }
       if (complete) {
@@ -862,7 +881,7 @@ __device__ __forceinline__ void attend_items(const CUtensorMap& map, const Atten
       }
     }
     if (!complete) {
-      if (threadIdx.x == 0) sh.open[n_open] = w;
+      if (threadIdx.x == 0) sh.open[n_open] = Part{w.b, w.h, w.first, w.parts, w.second};
       ++n_open;
     }
     if constexpr (SOLO) __syncwarp();      // the join's buffers are free again
@@ -876,13 +895,13 @@ __device__ __forceinline__ void attend_items(const CUtensorMap& map, const Atten
     __threadfence();
     __syncthreads();
     if (threadIdx.x < n_open) {
-      const Item& x = sh.open[threadIdx.x];
+      const Part& x = sh.open[threadIdx.x];
       sh.last[threadIdx.x] = atomicAdd(&sc.ticket[static_cast<int64_t>(x.b) * Hkv + x.h], 1) == x.parts - 1;
     }
     __syncthreads();
     for (int i_open = 0; i_open < n_open; ++i_open) {
       if (!sh.last[i_open]) continue;
-      const Item& x = sh.open[i_open];
+      const Part& x = sh.open[i_open];
       const int64_t orow = static_cast<int64_t>(x.b) * a.Hq + static_cast<int64_t>(x.h) * G;
       __threadfence();
       if (threadIdx.x == 0) sc.ticket[static_cast<int64_t>(x.b) * Hkv + x.h] = 0;
@@ -933,14 +952,16 @@ __global__ void __launch_bounds__(NW * 32, C::Geometry::CTAS)
 attend_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ AttendArgs a, const AttendScratch sc) {
   using G_ = typename C::Geometry;
   constexpr int D = C::kD, GP = C::kGP, KB = G_::KB, NST = G_::NST;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];     // the copies' swizzle needs 1024
+  uint8_t* smem = smem_raw;
+  // Four heads of 128 fp32 elements: the compiler keeps more loads on their way where it does not see that they are
+  // of shared memory (16 x 8192: 161 us, 176 us where it does; eight heads the other way, 286 and 266 us).
+  if (G_::F32 && D == 128 && GP == 4) asm volatile("" : "+l"(smem));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + NW * NST * (G_::STAGE + G_::SCALE) + NW * GP * (D + 4) * 4) + warp * NST;
-  __shared__ AttendShared sh;
+  auto& sh = *reinterpret_cast<typename G_::Shared*>(smem + NW * NST * (G_::STAGE + G_::SCALE) + NW * GP * D * 4 + G_::WEIGHTS);
   if (lane == 0) {
     if (!G_::F32) asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&map)) : "memory");
-    for (int s = 0; s < NST; ++s) mbar_init(&bars[s], 1);
+    for (int s = 0; s < NST; ++s) mbar_init(&sh.bars[warp][s], 1);
     mbar_fence_init();
   }
   __syncwarp();

@@ -266,7 +266,8 @@ KVPOP_HD bool next_part(W& w, const Split& sp, const Item& it, bool start, int c
 // leaves at most two partials per head: that of its range's first sequence,
 // and another.  Partial i of an item's sequence: by group, and whether its
 // range begins with this sequence.
-KVPOP_HD int64_t slot_of(const Item& x, int i, int Hkv) {
+template <typename X>
+KVPOP_HD int64_t slot_of(const X& x, int i, int Hkv) {
   return static_cast<int64_t>(2 * (x.first + i) + (i == 0 ? x.second : 0)) * Hkv + x.h;
 }
 
