@@ -62,8 +62,9 @@ __device__ __forceinline__ void turn_of(int pos, uint64_t step, float scale, flo
 // rounded reciprocal, q = x r is off by an ulp or so, and q + (x - q scale) r,
 // the remainder being exact in one FMA, is the rounded quotient (Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
-// 1990); compared with the division for every bf16 significand and 2^23 scales.
-// Below 2^-90 the remainder could underflow: those rows divide.
+// 1990).  The tests compare held bytes for every pair of bf16 significands, and
+// for fp32 rows under 25 factors.  Below 2^-90 the remainder could underflow:
+// those rows divide.
 template <int N>
 __device__ __forceinline__ void quotients(float (&x)[N], float scale) {
   if (scale == 0.f) {

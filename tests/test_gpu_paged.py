@@ -277,6 +277,60 @@ def test_e4m3_special_rows():
     assert (c.scales(0)[1, 0, 0, :2] == 0).all()
 
 
+def rows_of_every_quotient(exponent, rng):
+    """bf16 rows of 128: every significand as a row's largest element, 2^exponent
+    times, over every significand of the 19 exponents from there down (what the
+    scale brings below 2^-10 is held as zero), in float32."""
+    sig = np.arange(128, 256) / 128.0
+    small = (sig[None, :] * 2.0 ** -np.arange(0, 20)[:, None]).reshape(-1)
+    out = []
+    for m in sig:
+        x = rng.permutation(np.concatenate([small[small <= m], small[: -(small <= m).sum() % 127]]))
+        x = x.reshape(-1, 127) * rng.choice([-1, 1], size=(len(x) // 127, 127))
+        out.append(np.concatenate([x, np.full((len(x), 1), m)], 1))
+    return (np.concatenate(out) * 2.0 ** exponent).astype(np.float32)
+
+
+@pytest.mark.parametrize("exponent", [0, -82, -90, -100, 120])
+def test_e4m3_quotients_of_bf16_rows(exponent):
+    """Every pair of a row's largest element and an element that is not held as
+    zero, on both sides of 2^-90, where the quotients are formed differently."""
+    x = rows_of_every_quotient(exponent, np.random.default_rng(1))
+    n, d, page = len(x), 128, 256
+    t = torch.from_numpy(x).to(torch.bfloat16).cuda().view(1, n, 1, d)
+    assert np.array_equal(f64(t.float()).reshape(n, d), x.astype(np.float64))       # exact in bf16
+    held, scale = po.hold_e4m3(x)
+    slots, pos = torch.arange(n, dtype=torch.int32, device="cuda").view(1, n), torch.zeros(1, n, dtype=torch.int32, device="cuda")
+    rope = kp.make_rope(torch.empty(0, dtype=torch.float64, device="cuda"))
+    for step in (False, True):
+        c = cache_of(1, 1, d, page, -(-n // page), cache="e4m3")
+        if step:
+            c.append_qkv(0, rope, t, t, t, pos, slots, torch.empty_like(t))
+        else:
+            c.append(0, t, t, slots)
+        got = f64(c.pages(0).float())[:, 0].transpose(1, 0, 2, 3).reshape(2, -1, d)[:, :n]
+        gs = f64(c.scales(0))[:, 0].transpose(1, 0, 2).reshape(2, -1)[:, :n]
+        for kv in range(2):
+            assert np.array_equal(gs[kv], scale) and np.array_equal(got[kv], held)
+
+
+def test_e4m3_quotients_of_fp32_rows():
+    """Keys that append_qkv quantises from fp32: at position 0 without a norm they
+    are x times the rotation's scale, rounded to fp32 once."""
+    rng = np.random.default_rng(2)
+    x = rows_of_every_quotient(0, rng)
+    n, d, page = len(x), 128, 256
+    t = torch.from_numpy(x).to(torch.bfloat16).cuda().view(1, n, 1, d)
+    slots, pos = torch.arange(n, dtype=torch.int32, device="cuda").view(1, n), torch.zeros(1, n, dtype=torch.int32, device="cuda")
+    c = cache_of(1, 1, d, page, -(-n // page), cache="e4m3")
+    freq, qo = torch.ones(d // 2, dtype=torch.float64, device="cuda"), torch.empty_like(t)
+    for factor in rng.uniform(1, 2, size=25).astype(np.float32):
+        c.append_qkv(0, kp.make_rope(freq, scale=float(factor)), t, t, t, pos, slots, qo)
+        held, scale = po.hold_e4m3(x * factor)
+        got = f64(c.pages(0).float())[:, 0, 0].reshape(-1, d)[:n]
+        assert np.array_equal(f64(c.scales(0))[:, 0, 0].reshape(-1)[:n], scale) and np.array_equal(got, held)
+
+
 @pytest.mark.parametrize("dtype,cache,d,hq,hkv,rot,inter,b,n", [
     ("bf16", "native", 128, 8, 2, 128, False, 3, 21), ("bf16", "e4m3", 128, 8, 2, 128, False, 3, 21),
     ("bf16", "e4m3", 64, 5, 5, 24, False, 2, 17), ("bf16", "e4m3", 128, 3, 1, 64, True, 1, 16),
