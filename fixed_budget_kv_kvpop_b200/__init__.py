@@ -520,6 +520,8 @@ def make_rope(inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6, scal
         if w is not None:
             n = w.numel() if isinstance(w, torch.Tensor) else 0
             check_tensor(w, name, (n,), torch.float32, inv_freq.device)
+            if n == 0:
+                raise ValueError(f"{name}: empty (None: heads that are not normalised)")
             if w.data_ptr() % 16:
                 raise ValueError(f"{name}: must start on 16 bytes")
     if q_weight is not None and k_weight is not None and q_weight.numel() != k_weight.numel():

@@ -997,6 +997,13 @@ def test_refusals_on_the_gpu():
     assert torch.equal(c.pages(0), before) and c.get_error() == (kp.KVPOP_OK, 0)
 
 
+@pytest.mark.parametrize("name", ["q_weight", "k_weight"])
+def test_empty_norm_weights_are_refused(name):
+    """An empty tensor has no address: it would be taken for heads that are not normalised."""
+    with pytest.raises(ValueError, match=f"{name}: empty"):
+        kp.make_rope(torch.ones(32, dtype=torch.float64, device="cuda"), **{name: torch.empty(0, device="cuda")})
+
+
 # ---- together, and beside the fixed-budget cache ----
 
 def test_paged_decode_equals_a_budget_that_evicts_nothing():
