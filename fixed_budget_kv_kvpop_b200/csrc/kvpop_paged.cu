@@ -40,8 +40,10 @@ __device__ __forceinline__ uint32_t to_e4m3x4(const float* x) {
 
 // A frequency as the fraction of a turn per position, in units of 2^-64.
 // Products with a position wrap at whole turns, so the angle of any int32
-// position keeps all its bits (off by at most 2^-25 turns at 2^31, from the
-// frequency's own 53 bits), and no fp64 instruction is left per token: their
+// position keeps all its bits: off by at most 2^-32 turns from the cut to 32
+// bits, and at position 2^31 by 2^-23.6 turns more from the step's own rounding
+// for frequencies up to 1 (an fp64 product position * frequency is off by up to
+// 2^-24.6 turns there), in proportion below.  And no fp64 instruction is left per token: their
 // conversions ran at a sixteenth of the fp32 ones' rate and took 95% of the
 // conversion pipe's time.
 __device__ __forceinline__ uint64_t turn_step(double inv_freq) {

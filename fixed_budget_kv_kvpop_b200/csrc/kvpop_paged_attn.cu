@@ -7,20 +7,20 @@
 // neighbours in memory, are read at the same time.  The groups either take one
 // part of one sequence each, all parts as even as they come, or, where that
 // leaves the largest part well above the average, equal contiguous ranges of
-// all sequences' blocks (32 sequences of 16384 to 32768 tokens in 8 bits: 337
-// and 300 us; 16 of 8192 in fp32: 160 and 182 us).  Every CTA finds its range
+// all sequences' blocks (32 sequences of 16384 to 32768 tokens in 8 bits: 331
+// and 239 us; 16 of 8192 in fp32: 163 and 181 us).  Every CTA finds its range
 // from the lengths on the device.  Where the page table is so narrow that even
 // the longest sequences it can hold give no more parts of kMinShare blocks than
 // there are groups, those are the parts, and nothing is searched for: short
-// calls are a chain of latencies (117 tokens: 6.2 us so, 7.7 us searched).
+// calls are a chain of latencies (117 tokens: 5.5 us so, 6.1 us searched).
 // Many sequences of a few blocks each go, head by head, to single warps, which
-// then meet nobody (512 of 60 tokens: 38 us so, 71 us with a CTA for each).
+// then meet nobody (512 of 60 tokens: 38 us so, 72 us with a CTA for each).
 // Where a sequence lies in several ranges, each leaves a partial (accumulator,
 // running maximum, sum), and the CTA that arrives last joins them in their
 // order, so results do not depend on who is last.
 // Inside a CTA each warp has a ring of stages of its own: it copies block after
 // block into it by tensor copies (one instruction per 16 keys and values) and
-// computes on the oldest.  Warps meet once per item, to join their sums.
+// computes on the oldest, the next one or more being on their way.  Warps meet once per item, to join their sums.
 #include "kvpop_paged.cuh"
 #include "kvpop_paged_split.cuh"
 
@@ -185,9 +185,15 @@ struct Geo {
   static constexpr int MERGE = NW * GP * D * 4;              // accumulators that the warps of a CTA join
   static constexpr int WEIGHTS = F32 ? NW * KEYS * 16 : 0;   // fp32: weights of a piece for four heads
   // CTAs per SM.  More warps hide the chain from a block's arrival to its sums,
-  // up to where registers run out or power does: 64 x 8192 bf16 takes 338, 327
-  // and 314 us with 2, 3 and 4 CTAs in a short run, but 339, 336 and 359 us in
-  // a long one, where the GPU holds its 1000 W by its clock
+  // up to where registers run out: with 2 and with 3 CTAs 64 x 8192 bf16 takes
+  // 334 and 325 us, 32 x 32768 e4m3 284 and 240 us, 64 x 8192 fp32 of 64
+  // elements 173 and 178 us, 16 x 8192 fp32 of 128 164 and 179 us.  (In runs of
+  // a second the GPU holds its 1000 W by its clock, and most of that goes.)
+  // Above four heads three fit by spilling or with one stage, and the two ways
+  // are not far apart in either direction (8 heads: 64 x 8192 bf16 323 and
+  // 314 us, 64 x 1000 bf16 49 and 52; 16 heads: 64 x 8192 bf16 328 and 346,
+  // 16 x 8192 fp32 509 and 707) but for fp32 rows of 64 elements, where three
+  // would pay (64 x 8192 of 8 heads 311 and 231 us, of 16 heads 639 and 439)
   static constexpr int CTAS = GP > 4 ? 2 : F32 ? (D == 64 ? 3 : 2) : 3;
   // Stages of a warp's ring: as many as fit, two at least, so that a copy is on its way while a warp computes
   // (32 x 32768 e4m3 with four heads, where two just fit: 240 us, 264 us with one).  1 KB of each CTA's share is the system's.
@@ -230,7 +236,7 @@ __device__ __forceinline__ void write4(float* p, const float4& o, float L, bool 
 // its weight, and only bf16 holds every weight times every scale to the same
 // 16 bits.  (Values and weights in f16 take fewer instructions, but need one
 // reference for all weights of a warp, 2^31 below which a token is lost:
-// 32 x 32768 took 257 us so, 267 us in bf16.)
+// 32 x 32768 took 257 us so and 267 us in bf16 when a warp had one stage.)
 template <int D, bool E4M3, int GP>
 struct MmaPieces {
   using Geometry = Geo<__nv_bfloat16, D, E4M3, GP>;

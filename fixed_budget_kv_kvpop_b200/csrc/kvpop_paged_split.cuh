@@ -23,12 +23,12 @@
 
 namespace kvpop {
 
-constexpr int kMinShare = 8;             // blocks of a part at least (1 x 1024 tokens: 4 12.9 us, 8 11.7 us, 16 12.4 us, 32 17.3 us)
+constexpr int kMinShare = 8;             // blocks of a part at least (1 x 1024 tokens: 4 10.4 us, 8 9.3 us, 16 10.5 us, 32 12.9 us)
 constexpr int64_t kMostTokens = INT64_C(1) << 30;   // of a sequence
 // If there are more sequences than groups and none has more tokens than this, they go to single warps.  Few long ones
-// would leave warps idle (8 groups of 4 heads, bf16: 64 x 200 19 us against 25, 64 x 300 27 either way, 256 x 300 69
-// against 66; e4m3 64 x 400 34 against 30), the sooner the more a warp has to compute (fp32 on the FMA units, 8 groups
-// of 16 heads: 80 x 60 48 us against 60, 80 x 250 151 against 104).
+// would leave warps idle (8 groups of 4 heads, bf16: 64 x 200 20 us against 26, 64 x 300 26 against 28, 256 x 300 68
+// against 67; e4m3 64 x 400 33 against 31), the sooner the more a warp has to compute (fp32 on the FMA units, 8 groups
+// of 16 heads: 80 x 60 47 us against 53, 80 x 250 144 against 116).
 constexpr int solo_tokens(bool f32) { return f32 ? 64 : 256; }
 // Largest part that is taken for one part of one sequence per group, when equal
 // ranges would have `even` blocks: ranges cost a second item and its join.

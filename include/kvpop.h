@@ -413,8 +413,11 @@ typedef struct kvpop_rows {
  *   (a, b) -> (a cos - b sin, b cos + a sin), angle = position * inv_freq[i]
  * for the pairs i < rot_dim / 2: elements (i, i + rot_dim / 2), or with
  * interleaved (2i, 2i + 1); elements from rot_dim on are not turned.  Angles
- * are formed in fp64 (any int32 position), the rest in fp32, and the result
- * is rounded once.  rot_scale multiplies cosine and sine (1 for plain
+ * are formed as 64-bit fractions of a turn (any int32 position): for
+ * frequencies up to 1 they are off by at most 2^-32 turns, and at position p
+ * by p 2^-54.6 more.  The rest is fp32, the sum of squares too (elements
+ * beyond 2^60, or below 2^-60 with eps = 0, leave its range and are not
+ * normalised to the formula), and the result is rounded once.  rot_scale multiplies cosine and sine (1 for plain
  * rotation).  All pointers are device memory, read while the call runs. */
 typedef struct kvpop_rope {
   const float* q_weight;    /* fp32 [head_dim] or NULL, 16-byte aligned */
@@ -525,13 +528,20 @@ typedef struct kvpop_attend_options {
 
 /* Attention of one new token per sequence over its pages:
  *   s_j = scale q . k_j (capped),  out = sum_j softmax(s)_j v_j
- * over the tokens j < lens[b] (the last `window` of them), fp32 accumulation,
- * one launch; the work of all sequences is split evenly over the GPU along
+ * over the tokens j < lens[b] (the last `window` of them), one launch; the
+ * work of all sequences is split evenly over the GPU along
  * the cache's length and joined in a fixed order, so equal calls give equal
  * bits.  q, out: device [batch][n_q_heads][head_dim] in dtype, 16-byte
  * aligned, and out may be q; lse: device fp32 [batch][n_q_heads] receiving log sum_j e^(s_j),
  * or NULL.  page_table, lens as kvpop_paged_gather; 0 <= batch <= max_batch,
  * table_width * page_size <= 2^30.
+ * Scores, the softmax's statistics and all sums are fp32.  The weights of
+ * bf16 and e4m3 rows are held in 16 bits (two bf16 terms), so that each
+ * token's part of an element is right to 2^-16 of itself down to 2^-100, and
+ * bf16 outputs differ from those of fp32 weights in an occasional last place.
+ * Weights are relative to a running maximum that may lag by a factor of 2^8:
+ * attended values whose sum times 2^8 passes fp32's range (2^128), infinite
+ * ones among them, give infinities or NaN in their element.
  * A sequence with no token gets out = 0, lse = -inf.  Infinities and NaN in
  * tokens that are not attended do not reach the result; a NaN or +inf score
  * gives NaN.  A length that is negative or past table_width * page_size
