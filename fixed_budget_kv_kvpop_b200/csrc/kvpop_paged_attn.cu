@@ -33,7 +33,9 @@ namespace {
 
 constexpr int NW = 4;                    // warps per CTA
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kRaise = 8.f;            // a running maximum moves when a score passes it by this (in powers of two)
+// Weights are relative to a running maximum, kRaise (in powers of two) above the largest score when it was set: it
+// moves when a score passes it, so that no weight passes 1 and few scores move it.
+constexpr float kRaise = 8.f;
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -418,14 +420,14 @@ struct MmaPieces {
       top[r] = x[r][0];
 #pragma unroll
       for (int i = 1; i < 2 * NB; ++i) top[r] = fmaxf(top[r], x[r][i]);
-      raise |= top[r] > m[r] + kRaise;
+      raise |= top[r] > m[r];
     }
     if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float y = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
-        const float m1 = fmaxf(m[r], y);
+        const float m1 = fmaxf(m[r], y + kRaise);
         const float c = m[r] == -INFINITY ? 0.f : ex2(m[r] - m1);
         m[r] = m1;
         l[r] *= c;
@@ -617,10 +619,10 @@ struct FmaPieces {
         x[p] = key >= k_lo && key < k_hi ? f : -INFINITY;
         top = fmaxf(top, x[p]);
       }
-      if (__any_sync(0xffffffffu, top > m[c] + kRaise)) {
+      if (__any_sync(0xffffffffu, top > m[c])) {
         float y = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
         y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-        const float m1 = fmaxf(m[c], y);
+        const float m1 = fmaxf(m[c], y + kRaise);
         const float f = m[c] == -INFINITY ? 0.f : ex2(m[c] - m1);
         m[c] = m1;
         l[c] *= f;

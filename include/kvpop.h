@@ -539,9 +539,8 @@ typedef struct kvpop_attend_options {
  * bf16 and e4m3 rows are held in 16 bits (two bf16 terms), so that each
  * token's part of an element is right to 2^-16 of itself down to 2^-100, and
  * bf16 outputs differ from those of fp32 weights in an occasional last place.
- * Weights are relative to a running maximum that may lag by a factor of 2^8:
- * attended values whose sum times 2^8 passes fp32's range (2^128), infinite
- * ones among them, give infinities or NaN in their element.
+ * Attended values whose weighted sum passes fp32's range, infinite ones among
+ * them, give infinities or NaN in their element.
  * A sequence with no token gets out = 0, lse = -inf.  Infinities and NaN in
  * tokens that are not attended do not reach the result; a NaN or +inf score
  * gives NaN.  A length that is negative or past table_width * page_size

@@ -630,6 +630,21 @@ def test_attend_large_keys_and_small_queries(dtype, cache, d, g, hkv, page, ek, 
     check_attend(out[0], lse[0], q[0], x[:, :, 0], x[:, :, 1], dtype, scale)
 
 
+@pytest.mark.parametrize("dtype,cache,d,g,hkv,page", [SHAPES[0], SHAPES[3], SHAPES[5], SHAPES[7], SHAPES[8], SHAPES[9]])
+@pytest.mark.parametrize("n", [300, 2900])
+def test_attend_values_near_the_end_of_the_range(dtype, cache, d, g, hkv, page, n):
+    """Values of 2^116 whose scores lie 2^7.8 above those before them: their sum stays in fp32's range, 2^7.8 times it would not."""
+    c, table, q = filled([n], g * hkv, hkv, d, page, dtype, cache, seed=8)
+    q = (1 + torch.arange(g * hkv, device="cuda").view(1, -1, 1) / 1024).expand(1, -1, d).to(q.dtype).contiguous()
+    k, v = rows((1, n, hkv, d), dtype, 5, 0.01), rows((1, n, hkv, d), dtype, 6).abs() * 2.0 ** 116
+    k[:, n // 2:] += 5.4 / d ** 0.5
+    c.append(0, k, v, ints(slots_of(table, [n], page, n)))
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    c.attend(0, q, ints(table), ints([n]), out, lse)
+    x = held_rows(c, 0, table, n, page, 0)
+    check_attend(out[0], lse[0], q[0], x[:, :, 0], x[:, :, 1], dtype)
+
+
 @pytest.mark.parametrize("dtype,cache,hq,hkv", [("bf16", "native", 600, 600), ("bf16", "e4m3", 460, 460), ("f32", "native", 500, 500),
                                                  ("bf16", "native", 96, 6)])
 def test_attend_more_heads_than_the_gpu_has_blocks(dtype, cache, hq, hkv):
